@@ -6,6 +6,8 @@ no fallback: if the CUDA library is missing, every call raises.
 
 C-ABI entry points (same names here): ``moba_pool_keys``, ``moba_gate_topk``,
 ``moba_attn_fwd``, ``moba_fwd``, ``moba_workspace_size``, ``moba_kbar_elems``.
+The paged 8-bit KV cache: ``moba_cache_tables``, ``moba_cache_append``,
+``moba_cache_decode_fwd``, and ``MobaCache``, which owns one cache's buffers.
 """
 from __future__ import annotations
 
@@ -27,7 +29,10 @@ EXPORTS = ("moba_kbar_elems", "moba_workspace_size", "moba_pool_keys", "moba_gat
            "moba_launches_per_forward", "moba_read_device_error", "moba_status_string",
            "moba_last_error", "moba_gate_topk_noalloc", "moba_selftest_bounded_wait",
            "moba_host_staging_size", "moba_fwd_host", "moba_attn_naive", "moba_decode_workspace_size",
-           "moba_decode_fwd", "moba_pool_last_block", "moba_bwd_workspace_size", "moba_attn_bwd")
+           "moba_decode_fwd", "moba_pool_last_block", "moba_bwd_workspace_size", "moba_attn_bwd",
+           "moba_cache_tables", "moba_cache_append", "moba_cache_decode_workspace_size", "moba_cache_decode_fwd")
+
+CACHE_FORMATS = {"e4m3": 0, "int8": 1}
 
 
 class MobaError(RuntimeError):
@@ -49,6 +54,12 @@ class _CParams(ctypes.Structure):
         ("top_k", ctypes.c_int32),
         ("softmax_scale", ctypes.c_float),
     ]
+
+
+class _CCacheParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("max_seqs", "max_seqlen", "num_pages", "page_size", "num_q_heads", "num_kv_heads", "head_dim",
+                 "block_size", "top_k", "format")] + [("softmax_scale", ctypes.c_float)]
 
 
 def load():
@@ -96,6 +107,17 @@ def load():
         for f in ("moba_pool_keys", "moba_gate_topk", "moba_attn_fwd", "moba_fwd", "moba_route",
                   "moba_attn_past", "moba_attn_self_merge"):
             getattr(lib, f).restype = ctypes.c_int
+        C = ctypes.POINTER(_CCacheParams)
+        i64 = ctypes.c_int64
+        i32 = ctypes.c_int32
+        lib.moba_cache_tables.argtypes = [C] + [vp] * 9 + [i32, vp, vp]
+        lib.moba_cache_tables.restype = ctypes.c_int
+        lib.moba_cache_append.argtypes = [C, vp, i64, vp, i64, i32] + [vp] * 10
+        lib.moba_cache_append.restype = ctypes.c_int
+        lib.moba_cache_decode_workspace_size.argtypes = [C]
+        lib.moba_cache_decode_workspace_size.restype = sz
+        lib.moba_cache_decode_fwd.argtypes = [C] + [vp] * 10 + [sz, vp, vp, vp]
+        lib.moba_cache_decode_fwd.restype = ctypes.c_int
         lib.moba_selftest_bounded_wait.argtypes = [ctypes.POINTER(ctypes.c_int32)]
         lib.moba_selftest_bounded_wait.restype = ctypes.c_int
         lib.moba_read_device_error.argtypes = [ctypes.POINTER(ctypes.c_int32), ctypes.c_int]
@@ -286,6 +308,171 @@ def moba_selftest_bounded_wait() -> int:
     v = ctypes.c_int32(0)
     _check(load().moba_selftest_bounded_wait(ctypes.byref(v)))
     return int(v.value)
+
+
+class MobaCacheParams:
+    """Geometry of a paged 8-bit KV cache (moba_cache_params) and the shapes of its buffers."""
+
+    def __init__(self, max_seqs: int, max_seqlen: int, num_pages: int, page_size: int, num_q_heads: int,
+                 num_kv_heads: int, head_dim: int, block_size: int, top_k: int, format: str = "e4m3",
+                 softmax_scale: float = 0.0):
+        if format not in CACHE_FORMATS:
+            raise MobaError(2, "format must be one of %s (got %r)" % (", ".join(CACHE_FORMATS), format))
+        self.c = _CCacheParams(max_seqs, max_seqlen, num_pages, page_size, num_q_heads, num_kv_heads, head_dim,
+                               block_size, top_k, CACHE_FORMATS[format], softmax_scale)
+        self.format = format
+        self.workspace_bytes = int(load().moba_cache_decode_workspace_size(self.ref()))
+        if not self.workspace_bytes:
+            raise MobaError(2, load().moba_last_error().decode())
+        c = self.c
+        self.pages_per_seq = -(-max_seqlen // page_size)
+        self.max_blocks = -(-max_seqlen // block_size)
+        i32, f32 = "torch.int32", "torch.float32"
+        code = "torch.float8_e4m3fn" if format == "e4m3" else "torch.int8"
+        pool = (num_pages, num_kv_heads)
+        # dtype and shape of every buffer (None: any length)
+        self.buffers = {
+            "add": (i32, (max_seqs,)), "lens": (i32, (max_seqs,)), "lens_out": (i32, (max_seqs,)),
+            "tables": (i32, (max_seqs, self.pages_per_seq)), "free_pages": (i32, (num_pages,)),
+            "free_state": (i32, (2,)), "free_state_out": (i32, (2,)), "cu_new": (i32, (max_seqs + 1,)),
+            "slots": (i32, (None,)), "status": (i32, (1,)),
+            "K": ("torch.bfloat16", (None, num_kv_heads, head_dim)),
+            "V": ("torch.bfloat16", (None, num_kv_heads, head_dim)),
+            "Kc": (code, pool + (page_size, head_dim)), "Vc": (code, pool + (page_size, head_dim)),
+            "Ks": (f32, pool), "Vs": (f32, pool),
+            "Kbar": (f32, (max_seqs, self.max_blocks, num_kv_heads, head_dim)),
+            "Q": ("torch.bfloat16", (max_seqs, num_q_heads, head_dim)),
+            "O": ("torch.bfloat16", (max_seqs, num_q_heads, head_dim)),
+            "LSE": (f32, (max_seqs, num_q_heads)), "sel": (i32, (max_seqs, num_q_heads, top_k)),
+        }
+
+    def ref(self):
+        return ctypes.byref(self.c)
+
+    def check(self, device, **tensors):
+        """Every tensor has its dtype and shape, lies on `device` and is contiguous (K and V: in
+        their last two dimensions)."""
+        for name, t in tensors.items():
+            dtype, shape = self.buffers[name]
+            if str(t.dtype) != dtype:
+                raise MobaError(1, "%s must be %s (got %s)" % (name, dtype, t.dtype))
+            if len(t.shape) != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+                raise MobaError(1, "%s must have shape %s (got %s)" % (
+                    name, tuple("n" if w is None else w for w in shape), tuple(t.shape)))
+            if t.device != device:
+                raise MobaError(1, "%s is on %s, the call's tensors are on %s" % (name, t.device, device))
+            if name in ("K", "V"):
+                if t.shape[0] and (t.stride(2) != 1 or t.stride(1) != t.shape[2]):
+                    raise MobaError(1, "%s must be contiguous in its last two dimensions" % name)
+            elif not t.is_contiguous():
+                raise MobaError(1, "%s must be contiguous" % name)
+
+
+def _on(device, stream, call):
+    """Calls with `device` current, on the given stream or that device's current one."""
+    import torch
+    if device.type != "cuda":
+        raise MobaError(1, "the tensors must be on a CUDA device (got %s)" % device)
+    with torch.cuda.device(device):
+        _check(call(_stream(stream)))
+
+
+def moba_cache_tables(p: MobaCacheParams, add, lens, tables, free_pages, free_state, lens_out, free_state_out,
+                      cu_new, slots, status, stream=None) -> None:
+    """Block tables, slot map and free-page ring for the next step: add[s] new tokens for request s
+    (0: none, negative: it ends).  lens_out may be lens, free_state_out may be free_state."""
+    p.check(add.device, add=add, lens=lens, tables=tables, free_pages=free_pages, free_state=free_state,
+            lens_out=lens_out, free_state_out=free_state_out, cu_new=cu_new, slots=slots, status=status)
+    _on(add.device, stream, lambda st: load().moba_cache_tables(
+        p.ref(), _ptr(add), _ptr(lens), _ptr(tables), _ptr(free_pages), _ptr(free_state), _ptr(lens_out),
+        _ptr(free_state_out), _ptr(cu_new), _ptr(slots), slots.shape[0], _ptr(status), st))
+
+
+def moba_cache_append(p: MobaCacheParams, K, V, cu_new, lens, slots, tables, Kc, Vc, Ks, Vs, Kbar,
+                      stream=None) -> None:
+    """Writes the new tokens K, V [n, Hkv, D] (rows any multiple of 8 elements apart) into their
+    slots and pools the keys of blocks that become complete; lens are those after the step."""
+    p.check(K.device, K=K, V=V, cu_new=cu_new, lens=lens, slots=slots, tables=tables, Kc=Kc, Vc=Vc, Ks=Ks, Vs=Vs,
+            Kbar=Kbar)
+    n = K.shape[0]
+    if V.shape[0] != n or slots.shape[0] != n:
+        raise MobaError(1, "K, V and slots must have the same number of tokens (got %d, %d, %d)"
+                        % (n, V.shape[0], slots.shape[0]))
+    row = p.c.num_kv_heads * p.c.head_dim
+    ks, vs = (K.stride(0), V.stride(0)) if n > 1 else (row, row)
+    _on(K.device, stream, lambda st: load().moba_cache_append(
+        p.ref(), _ptr(K), ks, _ptr(V), vs, n, _ptr(cu_new), _ptr(lens), _ptr(slots), _ptr(tables), _ptr(Kc),
+        _ptr(Vc), _ptr(Ks), _ptr(Vs), _ptr(Kbar), st))
+
+
+def moba_cache_decode_workspace_size(p: MobaCacheParams) -> int:
+    return p.workspace_bytes
+
+
+def moba_cache_decode_fwd(p: MobaCacheParams, Q, Kc, Vc, Ks, Vs, Kbar, lens, tables, workspace, O, LSE, sel=None,
+                          stream=None) -> None:
+    """Gated decode: Q [max_seqs, Hq, D] (the newest token of each request) against the paged 8-bit
+    cache; O [max_seqs, Hq, D], LSE [max_seqs, Hq], and sel [max_seqs, Hq, top_k] if given."""
+    p.check(Q.device, Q=Q, Kc=Kc, Vc=Vc, Ks=Ks, Vs=Vs, Kbar=Kbar, lens=lens, tables=tables, O=O, LSE=LSE)
+    if sel is not None:
+        p.check(Q.device, sel=sel)
+    if workspace.device != Q.device or not workspace.is_contiguous():
+        raise MobaError(1, "workspace must be contiguous and on %s" % Q.device)
+    _on(Q.device, stream, lambda st: load().moba_cache_decode_fwd(
+        p.ref(), _ptr(Q), _ptr(Kc), _ptr(Vc), _ptr(Ks), _ptr(Vs), _ptr(Kbar), _ptr(lens), _ptr(tables), _ptr(sel),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(O), _ptr(LSE), st))
+
+
+def alloc_cache_workspace(p: MobaCacheParams, device="cuda"):
+    import torch
+    return torch.empty(p.workspace_bytes, dtype=torch.uint8, device=device)
+
+
+class MobaCache:
+    """The paged 8-bit KV cache of one layer: its pool, with the block tables, lengths and free
+    pages of up to ``max_seqs`` requests.  A step is ``extend`` (how many tokens each request
+    gets), ``append`` (their keys and values) and ``decode``.  The calls run on the current stream
+    and enqueue kernels only, so a step can be captured into a CUDA graph.  (More layers share the
+    tables and lengths: call the functions with each layer's pool.)"""
+
+    def __init__(self, p: MobaCacheParams, device="cuda"):
+        import torch
+        self.p, self.device = p, torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+
+        def zeros(name):
+            dtype, shape = p.buffers[name]
+            return torch.zeros(shape, dtype=getattr(torch, dtype[6:]), device=self.device)
+
+        self.Kc, self.Vc, self.Ks, self.Vs, self.Kbar = (zeros(n) for n in ("Kc", "Vc", "Ks", "Vs", "Kbar"))
+        self.lens, self.tables, self.cu_new, self.status = (zeros(n) for n in ("lens", "tables", "cu_new", "status"))
+        self.free_pages = torch.arange(p.c.num_pages, dtype=torch.int32, device=self.device)
+        self.free_state = torch.tensor([0, p.c.num_pages], dtype=torch.int32, device=self.device)
+        self.workspace = alloc_cache_workspace(p, self.device)
+
+    def extend(self, add, max_tokens: int):
+        """Tables and slots for add[s] new tokens a request (negative: it ends), at most
+        ``max_tokens`` in all.  Returns the slot map; ``status`` tells whether it was done."""
+        import torch
+        slots = torch.empty(max_tokens, dtype=torch.int32, device=self.device)
+        moba_cache_tables(self.p, add, self.lens, self.tables, self.free_pages, self.free_state, self.lens,
+                          self.free_state, self.cu_new, slots, self.status)
+        return slots
+
+    def append(self, K, V, slots) -> None:
+        """The new tokens' keys and values, packed in the order of the requests."""
+        moba_cache_append(self.p, K, V, self.cu_new, self.lens, slots, self.tables, self.Kc, self.Vc, self.Ks,
+                          self.Vs, self.Kbar)
+
+    def decode(self, Q, sel=None):
+        """(O, LSE) of the newest token of every request."""
+        import torch
+        O = torch.empty_like(Q)
+        LSE = torch.empty(Q.shape[:2], dtype=torch.float32, device=self.device)
+        moba_cache_decode_fwd(self.p, Q, self.Kc, self.Vc, self.Ks, self.Vs, self.Kbar, self.lens, self.tables,
+                              self.workspace, O, LSE, sel=sel)
+        return O, LSE
 
 
 def alloc_workspace(p: MobaParams, device="cuda"):

@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "moba.h"
+#include "api_common.cuh"
 #include "moba_internal.cuh"
 #include "sm100.cuh"
 
@@ -198,6 +199,25 @@ moba_status check_ws(const moba::Geom& g, void* ws, size_t bytes, moba::Work* w)
   carve(g, (char*)ws, w);
   return MOBA_OK;
 }
+
+}  // namespace
+
+// The pieces of this layer that cache_api.cu shares.
+namespace moba {
+namespace api {
+void clear_error() { g_err[0] = 0; }
+moba_status fail_with(moba_status st, const char* msg) { return fail(st, "%s", msg); }
+moba_status cuda_error(cudaError_t e, const char* where) { return cuda_fail(e, where); }
+moba_status device_error_word(int** err) {
+  Geom g;
+  const moba_status st = check_device(&g);
+  if (st == MOBA_OK) *err = g.err;
+  return st;
+}
+}  // namespace api
+}  // namespace moba
+
+namespace {
 
 #define MOBA_TRY(x)                      \
   do {                                   \

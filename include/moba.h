@@ -268,13 +268,120 @@ MOBA_API moba_status moba_fwd_host(const moba_params* p, const void* Q, const vo
                                    float* LSE, void* staging, size_t staging_bytes, void* const* streams,
                                    int nstreams);
 
+/*
+ * Paged 8-bit KV cache, and gated decode over it.
+ *
+ * A pool of `num_pages` pages holds the keys and values of up to `max_seqs` requests (the cached
+ * pages of one request in any order, named by its row of the block tables):
+ *   Kc, Vc  [num_pages, Hkv, page_size, D]  8-bit codes (e4m3 or int8)
+ *   Ks, Vs  [num_pages, Hkv] fp32           a scale for each page and KV head: value = code * scale
+ *   tables  [max_seqs, ceil(max_seqlen / page_size)] int32: page of each run of page_size tokens
+ *   lens    [max_seqs] int32                cached tokens of each request (0: the slot is free)
+ *   Kbar    [max_seqs, ceil(max_seqlen / block_size), Hkv, D] fp32: mean of the stored keys
+ *           (code * scale) of each complete MoBA block
+ * All of these are DEVICE buffers of the caller; lengths live on the device only, so that a
+ * captured CUDA graph of tables -> append -> decode serves step after step.  Int32 vectors need
+ * 4-byte alignment, everything else 16.  A captured call uses the buffers it was captured with:
+ * two graphs that share a workspace, or a cache, must not run at the same time.
+ *
+ * A page id outside [0, num_pages), a length outside [0, max_seqlen] and a slot that does not
+ * fit its token never lead to an access: such tokens are left out (read as masked, not written),
+ * and page ids and slots set bit 2 of the device error word (moba_read_device_error).  A negative
+ * slot is skipped without an error.
+ */
+typedef enum {
+  MOBA_CACHE_E4M3 = 0, /* fp8 e4m3: values to 4 significant bits, largest code 448 */
+  MOBA_CACHE_INT8 = 1  /* -127..127 */
+} moba_cache_format;
+
+typedef struct {
+  int32_t max_seqs;      /* request slots, 1..65535 */
+  int32_t max_seqlen;    /* tokens that one request may hold, 1..2^30 */
+  int32_t num_pages;     /* pages in the pool */
+  int32_t page_size;     /* tokens of a page: 16, 32, 64 or 128 */
+  int32_t num_q_heads;   /* Hq, a multiple of num_kv_heads */
+  int32_t num_kv_heads;  /* Hkv */
+  int32_t head_dim;      /* D: 64 or 128 */
+  int32_t block_size;    /* MoBA block: a multiple of 128, at most 8192 */
+  int32_t top_k;         /* blocks per query including its own block: 1..16 */
+  int32_t format;        /* moba_cache_format */
+  float softmax_scale;   /* <= 0 means 1/sqrt(head_dim) */
+} moba_cache_params;
+
+/*
+ * Block tables, slot map and free-page ring for the next step, from the requests' lengths.
+ *   add    [max_seqs]: add[s] > 0: request s gets that many new tokens; 0: it stays as it is;
+ *          < 0: it ends, its pages go back and its length becomes 0.
+ *   lens   [max_seqs] cached tokens before the call;  lens_out  the same after it.
+ *   tables: entries of the pages that a request grows into are written, all others are left.
+ *   free_pages [num_pages], free_state [2] = {head, count}: a ring; the free pages are
+ *          free_pages[(head + i) mod num_pages], i < count.  Requests take from its front, in
+ *          the order of s and of the pages in a request; pages that come back go behind its end,
+ *          in the same order, and can be taken from the next call on.  free_state_out: after it.
+ *   cu_new [max_seqs + 1] out: offsets of each request's new tokens in the packed step.
+ *   slots  [max_tokens] out: page * page_size + offset of each new token, -1 behind the last
+ *          (-1 too where the ring held a page id outside the pool).
+ *   status [1] out: 0, or the sum of 1 (too few free pages), 2 (a request would exceed
+ *          max_seqlen), 4 (more new tokens than max_tokens), 8 (a length or free_state outside
+ *          its range, or more pages given back than the ring has room for).  With a status other
+ *          than 0 nothing changes: lens_out = lens, free_state_out = free_state, cu_new is all 0
+ *          and slots all -1, so that the append that follows writes nothing.
+ * lens_out may be lens and free_state_out may be free_state (in place); other buffers must not
+ * overlap.  All values are exact and do not depend on timing.
+ */
+MOBA_API moba_status moba_cache_tables(const moba_cache_params* p, const int32_t* add, const int32_t* lens,
+                                       int32_t* tables, int32_t* free_pages, const int32_t* free_state,
+                                       int32_t* lens_out, int32_t* free_state_out, int32_t* cu_new, int32_t* slots,
+                                       int32_t max_tokens, int32_t* status, void* stream);
+
+/*
+ * Writes the new tokens' keys and values into their slots.
+ *   K, V     [max_tokens, Hkv, D] bf16, the requests' new tokens packed in the order of s; rows
+ *            k_stride (v_stride) elements apart, a multiple of 8 and at least Hkv * D (K and V
+ *            may be slices of one projection).  Rows behind cu_new[max_seqs] are not read.
+ *   cu_new, slots  from moba_cache_tables;  lens  the lengths AFTER the step (its lens_out).
+ *   Scale of a (page, KV head) with qmax = 448 (e4m3) or 127 (int8): the least number of 8
+ *   significant bits that is >= max(2^-96, max |x|) / qmax over the finite new values, or the old
+ *   scale if the page held tokens and that is larger.  When a page's scale grows, its older codes
+ *   are moved to it (code * old / new, to nearest).  Codes are x / scale to the nearest, ties to
+ *   even, clamped to +-qmax; a NaN stays NaN in e4m3 and becomes 0 in int8.
+ *   Kbar: the pooled key of each block whose last token is among the new ones is written; the
+ *   other blocks are left.
+ * Writing the same step again changes nothing more.
+ */
+MOBA_API moba_status moba_cache_append(const moba_cache_params* p, const void* K, int64_t k_stride, const void* V,
+                                       int64_t v_stride, int32_t max_tokens, const int32_t* cu_new,
+                                       const int32_t* lens, const int32_t* slots, const int32_t* tables, void* Kc,
+                                       void* Vc, float* Ks, float* Vs, float* Kbar, void* stream);
+
+/*
+ * Gated decode over the paged 8-bit cache: moba_decode_fwd's rule (own block up to the newest
+ * token, plus the top_k - 1 earlier blocks with the largest <q, Kbar[b]>, ties to the lower
+ * block) on the stored values code * scale.
+ *   Q     [max_seqs, Hq, D] bf16: the query of each request's newest token (position lens - 1).
+ *   lens, tables, Kc, Vc, Ks, Vs, Kbar: the cache, which INCLUDES the newest token.  Only the
+ *         blocks of Kbar before each request's last block are read.
+ *   sel   [max_seqs, Hq, top_k] int32 out, as for moba_gate_topk; may be NULL.  Scores are summed
+ *         in fp64; one that is NaN ranks last.
+ *   workspace: >= moba_cache_decode_workspace_size(p) bytes, 256-byte aligned.
+ *   O     [max_seqs, Hq, D] bf16 out;  LSE [max_seqs, Hq] fp32 out.
+ *   A request of length 0 gets sel = -1, O = 0 and LSE = -inf.
+ * Whatever stands in a page behind the newest token is without effect.
+ */
+MOBA_API size_t moba_cache_decode_workspace_size(const moba_cache_params* p);
+MOBA_API moba_status moba_cache_decode_fwd(const moba_cache_params* p, const void* Q, const void* Kc, const void* Vc,
+                                           const float* Ks, const float* Vs, const float* Kbar, const int32_t* lens,
+                                           const int32_t* tables, int32_t* sel, void* workspace,
+                                           size_t workspace_bytes, void* O, float* LSE, void* stream);
+
 /* Kernel launches one moba_fwd enqueues for these params (host only; -1 if invalid). */
 MOBA_API int moba_launches_per_forward(const moba_params* p);
 
 /*
  * Device error word of the current device: the tensor-core kernels bound every wait on an
  * mbarrier (about 2 s); a wait that gives up ORs 1 into this word and the kernel returns
- * early instead of hanging.  Reads it synchronously (and zeroes it when `clear` != 0).
+ * early instead of hanging.  The paged-cache kernels OR 2 into it for a page id or slot outside
+ * the pool (see there).  Reads it synchronously (and zeroes it when `clear` != 0).
  * A non-zero value means the outputs of the affected launches are not valid.
  */
 MOBA_API moba_status moba_read_device_error(int32_t* value, int clear);
