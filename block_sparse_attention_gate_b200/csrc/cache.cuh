@@ -69,15 +69,27 @@ __device__ __forceinline__ uint32_t float2_to_codes2(float a, float b) {
   }
 }
 
-// Work space of one decode call (device pointers).
+// A block that heads of one tile of 8 chose: byte h of slots is head h's slot, 0xff if it did not.
+struct __align__(16) CacheSeg {
+  int32_t block;
+  int32_t pad;
+  uint32_t slots[2];
+};
+
+// Work space of one decode call (device pointers), and how its blocks are cut.  An entry of the work
+// list is a (request, KV head, tile of 8 heads), its units are chunks of CK keys.
 struct CacheDecodeWork {
   double* score;     // [B, Hq, MB] gate scores
-  float* part_o;     // [B, Hq, k, D] partial outputs
-  float* part_lse;   // [B, Hq, k]
+  CacheSeg* segs;    // [entries, max_segs] distinct blocks, the own one first
+  int32_t* units;    // [entries] chunks in all
+  float* part_o;     // [B, Hq, k, NC, D] partial sums of weighted values
+  float2* part_ml;   // [B, Hq, k, NC] running maximum (log2 units), sum of the softmax
   int32_t* sel;      // [B, Hq, k] (used when the caller passes none)
+  int32_t max_segs, CK, NC;
   size_t bytes;
 };
 
+int cache_chunk_keys(const CacheGeom& g);
 cudaError_t launch_cache_tables(const CacheGeom& g, const int32_t* add, const int32_t* lens, int32_t* tables,
                                 int32_t* free_pages, const int32_t* free_state, int32_t* lens_out,
                                 int32_t* free_state_out, int32_t* cu_new, int32_t* slots, int32_t max_tokens,

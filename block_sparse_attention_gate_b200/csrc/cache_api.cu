@@ -57,6 +57,8 @@ moba_status make_cache_geom(const moba_cache_params* p, moba::CacheGeom* g) {
   const int64_t MP = ((int64_t)p->max_seqlen + p->page_size - 1) / p->page_size;
   const int64_t MB = ((int64_t)p->max_seqlen + p->block_size - 1) / p->block_size;
   if (MB > 16384) return fail(MOBA_ERR_UNSUPPORTED, "more than 16384 blocks in one request");
+  if ((int64_t)p->num_pages * p->num_kv_heads > kI32Max)
+    return fail(MOBA_ERR_UNSUPPORTED, "num_pages * num_kv_heads exceeds 2^31-1");
   if (MP * p->max_seqs > kI32Max) return fail(MOBA_ERR_UNSUPPORTED, "max_seqs * pages of a request exceeds 2^31-1");
   if ((int64_t)p->max_seqs * p->num_q_heads * p->top_k > kI32Max)
     return fail(MOBA_ERR_UNSUPPORTED, "max_seqs * num_q_heads * top_k exceeds 2^31-1");
@@ -76,6 +78,10 @@ moba_status make_cache_geom(const moba_cache_params* p, moba::CacheGeom* g) {
   g->scale = p->softmax_scale > 0.f ? p->softmax_scale : 1.0f / sqrtf((float)p->head_dim);
   g->scale_log2 = g->scale * 1.4426950408889634f;
   g->err = nullptr;
+  const int ck = moba::cache_chunk_keys(*g);
+  const int64_t past = MB - 1 < 8 * (p->top_k - 1) ? MB - 1 : 8 * (p->top_k - 1);
+  if ((1 + past) * ((p->block_size + ck - 1) / ck) * p->max_seqs * p->num_kv_heads * ((g->G + 7) / 8) > kI32Max)
+    return fail(MOBA_ERR_UNSUPPORTED, "more than 2^31-1 chunks of chosen blocks");
   return MOBA_OK;
 }
 
@@ -92,12 +98,19 @@ moba::CacheDecodeWork carve_cache_decode(const moba::CacheGeom& g, char* base) {
     off += (bytes + 255) & ~(size_t)255;
     return ptr;
   };
-  const size_t rows = (size_t)g.B * g.Hq, units = rows * g.k;
   moba::CacheDecodeWork w;
-  w.score = (double*)take(rows * g.MB * sizeof(double));
-  w.part_o = (float*)take(units * g.D * sizeof(float));
-  w.part_lse = (float*)take(units * sizeof(float));
-  w.sel = (int32_t*)take(units * sizeof(int32_t));
+  w.CK = moba::cache_chunk_keys(g);
+  w.NC = (g.bs + w.CK - 1) / w.CK;
+  const int past = 8 * (g.k - 1);  // distinct earlier blocks that 8 heads can choose
+  w.max_segs = 1 + (past < g.MB - 1 ? past : g.MB - 1);
+  const size_t rows = (size_t)g.B * g.Hq, parts = rows * g.k * w.NC;
+  const size_t entries = (size_t)g.B * g.Hkv * ((g.G + 7) / 8);
+  w.score = (double*)take(g.k > 1 ? rows * g.MB * sizeof(double) : 0);
+  w.segs = (moba::CacheSeg*)take(entries * w.max_segs * sizeof(moba::CacheSeg));
+  w.units = (int32_t*)take(entries * sizeof(int32_t));
+  w.part_o = (float*)take(parts * g.D * sizeof(float));
+  w.part_ml = (float2*)take(parts * sizeof(float2));
+  w.sel = (int32_t*)take(rows * g.k * sizeof(int32_t));
   w.bytes = off;
   return w;
 }

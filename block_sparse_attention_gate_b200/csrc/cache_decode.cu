@@ -3,196 +3,784 @@
 // the top_k - 1 earlier blocks with the largest <q, Kbar[b]>, ties to the lower block:
 //   z_j = scale * <q, code_j> * Ks[page(j)],  O = sum_j softmax(z)_j * code'_j * Vs[page(j)],
 //   LSE = log sum_j exp(z_j).   A request of length 0 gets O = 0, LSE = -inf, no blocks.
-// The gate's outcome is discrete, so its scores are summed in 64 bits (bf16 times fp32 is exact
-// there): the choice is that of the exact scores but for ties to 2^-50.
+//
+//   cache_gate_kernel : scores and choice of every head of a (request, KV head), and the list of
+//                       the distinct blocks that those heads chose.
+//   cache_attn_kernel : each distinct block is read once for all the heads (up to 8) that chose
+//                       it, in chunks of CK keys spread evenly over the warps of a persistent grid.
+//   cache_merge_kernel: the chunks' partial results of a (request, head), by online softmax.
+//
+// Bound by HBM: the chosen blocks' codes, 2 D bytes a key and KV head.
+#include <cudaTypedefs.h>
 #include <float.h>
 
 #include "cache.cuh"
+#include "sm100.cuh"
 
 namespace moba {
 namespace {
 
 constexpr float kLn2C = 0.6931471805599453f;
 
+// ------------------------------------------------------------------------------------ gate
+//
+// The gate's outcome is discrete, so its scores are summed in 64 bits (bf16 times fp32 is exact
+// there): the choice is that of the exact scores but for ties to about 2^-50.
+
+constexpr int kGateWarps = 8;
+
 __device__ __forceinline__ bool ranks_before(double sa, int32_t ba, double sb, int32_t bb) {
   return sa > sb || (sa == sb && ba < bb);
 }
 
-// One CTA per (request, KV head): scores of the group's heads, then one warp a head picks.
-template <int kD>
-__global__ void __launch_bounds__(256)
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Sum of v[x] over the warp's lanes, for all 32 x at once: lane x returns the sum of v[x].  Each
+// step halves the values a lane still carries: 31 exchanges instead of 5 for every value.
+__device__ __forceinline__ double warp_sums(double (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int half = 16; half >= 1; half >>= 1) {
+    const bool up = (lane & half) != 0;
+#pragma unroll
+    for (int x = 0; x < half; ++x) {
+      const double give = up ? v[x] : v[x + half], keep = up ? v[x + half] : v[x];
+      v[x] = keep + __shfl_xor_sync(0xffffffffu, give, half);
+    }
+  }
+  return v[0];
+}
+
+// The cluster of a (request, KV head): its CTAs share the earlier blocks' scores (kH heads and
+// 32 / kH blocks a warp at a time, a lane per D / 32 dimensions), then CTA 0 chooses, a warp a
+// head, and lists the distinct blocks of every 8 heads.
+template <int kD, int kH>
+__global__ void __launch_bounds__(kGateWarps * 32)
     cache_gate_kernel(CacheGeom g, const __nv_bfloat16* __restrict__ Q, const float* __restrict__ Kbar,
-                      const int32_t* __restrict__ lens, double* score, int32_t* __restrict__ sel) {
-  constexpr int kDL = kD / 32;
-  const int gk = blockIdx.x, s = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+                      const int32_t* __restrict__ lens, int32_t* __restrict__ sel, CacheDecodeWork w) {
+  constexpr int kDL = kD / 32, kR = 32 / kH;
+  __shared__ int32_t s_sel[8][kMaxTopK];
+  const int rank = blockIdx.x, gk = blockIdx.y, s = blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t len = cached_len(g, lens, s);
   const int i = len > 0 ? (len - 1) / g.bs : -1;
-  for (int b = warp; b < i; b += 8) {
-    float kb[kDL];
+  const size_t row0 = (size_t)s * g.Hq + (size_t)gk * g.G;
+  if (g.k > 1) {
+    for (int h0 = 0; h0 < g.G; h0 += kH) {
+      double q[kH][kDL];
 #pragma unroll
-    for (int x = 0; x < kDL; ++x) kb[x] = __ldg(Kbar + (((size_t)s * g.MB + b) * g.Hkv + gk) * kD + lane + 32 * x);
-    for (int hh = 0; hh < g.G; ++hh) {
-      const size_t row = (size_t)s * g.Hq + gk * g.G + hh;
-      double acc = 0.0;
+      for (int h = 0; h < kH; ++h)
 #pragma unroll
-      for (int x = 0; x < kDL; ++x)
-        acc = fma((double)__bfloat162float(Q[row * kD + lane + 32 * x]), (double)kb[x], acc);
+        for (int x = 0; x < kDL; ++x)
+          q[h][x] = h0 + h < g.G ? (double)__bfloat162float(Q[(row0 + h0 + h) * kD + lane * kDL + x]) : 0.0;
+      for (int b0 = (rank * kGateWarps + warp) * kR; b0 < i; b0 += gridDim.x * kGateWarps * kR) {
+        float kb[kR][kDL];
 #pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-      if (lane == 0) score[row * g.MB + b] = acc == acc ? acc : -INFINITY;  // NaN ranks last
+        for (int r = 0; r < kR; ++r) {
+          const float* src = Kbar + (((size_t)s * g.MB + b0 + r) * g.Hkv + gk) * kD + lane * kDL;
+          if (b0 + r < i) {
+            if constexpr (kDL == 4) {
+              const float4 f = __ldg(reinterpret_cast<const float4*>(src));
+              kb[r][0] = f.x, kb[r][1] = f.y, kb[r][2] = f.z, kb[r][3] = f.w;
+            } else {
+              const float2 f = __ldg(reinterpret_cast<const float2*>(src));
+              kb[r][0] = f.x, kb[r][1] = f.y;
+            }
+          } else {
+#pragma unroll
+            for (int x = 0; x < kDL; ++x) kb[r][x] = 0.f;
+          }
+        }
+        double v[32];
+#pragma unroll
+        for (int r = 0; r < kR; ++r)
+#pragma unroll
+          for (int h = 0; h < kH; ++h) {
+            double acc = 0.0;
+#pragma unroll
+            for (int x = 0; x < kDL; ++x) acc = fma(q[h][x], (double)kb[r][x], acc);
+            v[r * kH + h] = acc;
+          }
+        const double sum = warp_sums(v);
+        const int r = lane / kH, h = lane % kH;
+        if (b0 + r < i && h0 + h < g.G)
+          w.score[(row0 + h0 + h) * g.MB + b0 + r] = sum == sum ? sum : -INFINITY;  // NaN ranks last
+      }
     }
+    if (gridDim.x > 1) cluster_barrier(); else __syncthreads();
   }
-  __syncthreads();
-  const int m = min(g.k - 1, max(i, 0));
-  for (int hh = warp; hh < g.G; hh += 8) {
-    const size_t row = (size_t)s * g.Hq + gk * g.G + hh;
-    int32_t* out = sel + row * g.k;
-    if (lane == 0) out[0] = i;
-    double last = INFINITY;
-    int32_t last_b = -1;
-    for (int q = 0; q < m; ++q) {
-      double bs_ = -INFINITY;
-      int32_t bb = INT32_MAX;
-      for (int b = lane; b < i; b += 32) {
-        const double v = score[row * g.MB + b];
-        if (ranks_before(last, last_b, v, b) && ranks_before(v, b, bs_, bb)) { bs_ = v; bb = b; }
-      }
+  if (rank != 0) return;
+  const int m = min(g.k - 1, max(i, 0)), HT = (g.G + 7) / 8;
+  for (int ht = 0; ht < HT; ++ht) {
+    const int hh = ht * 8 + warp, heads = min(8, g.G - ht * 8);
+    if (hh < g.G) {
+      const double* sc = w.score + (row0 + hh) * g.MB;
+      int32_t mine = lane == 0 ? i : -1;  // this lane's entry of the row of sel
+      double last = INFINITY;
+      int32_t last_b = -1;
+      for (int q = 0; q < m; ++q) {
+        double best = -INFINITY;
+        int32_t bb = INT32_MAX;
+        for (int b = lane; b < i; b += 32) {
+          const double v = sc[b];
+          if (ranks_before(last, last_b, v, b) && ranks_before(v, b, best, bb)) { best = v; bb = b; }
+        }
 #pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) {
-        const double os = __shfl_xor_sync(0xffffffffu, bs_, off);
-        const int32_t ob = __shfl_xor_sync(0xffffffffu, bb, off);
-        if (ranks_before(os, ob, bs_, bb)) { bs_ = os; bb = ob; }
+        for (int off = 16; off >= 1; off >>= 1) {
+          const double os = __shfl_xor_sync(0xffffffffu, best, off);
+          const int32_t ob = __shfl_xor_sync(0xffffffffu, bb, off);
+          if (ranks_before(os, ob, best, bb)) { best = os; bb = ob; }
+        }
+        if (lane == 1 + q) mine = bb;
+        last = best;
+        last_b = bb;
       }
-      if (lane == 0) out[1 + q] = bb;
-      last = bs_;
-      last_b = bb;
+      if (lane < g.k) {
+        sel[(row0 + hh) * g.k + lane] = mine;
+        s_sel[warp][lane] = mine;
+      }
     }
-    for (int q = 1 + m + lane; q < g.k; q += 32) out[q] = -1;
+    __syncthreads();
+    if (warp == 0) {
+      const size_t idx = ((size_t)s * g.Hkv + gk) * HT + ht;
+      CacheSeg* segs = w.segs + idx * w.max_segs;
+      // the own block is every head's slot 0; heads beyond the group take nothing
+      if (lane == 0 && i >= 0) {
+        CacheSeg own{i, 0, {~0u, ~0u}};
+        for (int h = 0; h < heads; ++h) own.slots[h >> 2] &= ~(0xffu << 8 * (h & 3));
+        segs[0] = own;
+      }
+      int count = i >= 0 ? 1 : 0;
+      const int n = heads * m;  // chosen (head, slot) pairs, head by head
+      for (int e0 = 0; e0 < n; e0 += 32) {
+        const int e = e0 + lane, h = e / max(m, 1);
+        const int32_t b = e < n ? s_sel[h][1 + e % m] : -1;
+        bool first = e < n;
+        CacheSeg seg{b, 0, {~0u, ~0u}};
+        if (e < n)
+          for (int o = 0; o < n; ++o) {
+            const int oh = o / m, oj = 1 + o % m;
+            if (s_sel[oh][oj] == b) {
+              if (o < e) first = false;
+              seg.slots[oh >> 2] &= ~(0xffu << 8 * (oh & 3)) | (uint32_t)oj << 8 * (oh & 3);
+            }
+          }
+        const uint32_t firsts = __ballot_sync(0xffffffffu, first);
+        if (first) segs[count + __popc(firsts & ((1u << lane) - 1))] = seg;
+        count += __popc(firsts);
+      }
+      if (lane == 0) {
+        const int own_n = len - max(i, 0) * g.bs;  // 0 where the request is empty
+        w.units[idx] = count ? (own_n + w.CK - 1) / w.CK + (count - 1) * w.NC : 0;
+      }
+    }
+    __syncthreads();
   }
 }
 
-// One CTA per (slot, query head, request): a warp takes every fourth key, a lane D/32 dimensions.
+// ------------------------------------------------------------------------------- attention
+//
+// Every warp works alone: it has a ring of kStages tiles of 32 keys (keys and values, by TMA) and
+// takes a contiguous run of the units (chunks of CK keys of a distinct block).  One query for each
+// of up to 8 heads: S = K Q^T and O += V^T P on mma.m16n8k16, with keys (dimensions) as the 16
+// rows and the heads as the 8 columns, so that the codes, converted in registers to fp16 (exact),
+// are the large operand and nothing is padded.  tcgen05 has nothing to win here: its operands would
+// have to be converted and written back to shared memory first, and the tile's arithmetic is a
+// quarter of what the legacy instructions do in the time that the codes take to arrive.
+//  - Q is scaled by a power of two for each head and held in fp16: exact down to 2^-32 of the head's
+//    largest element.
+//  - The value scale enters through the exponent, w_j = 2^(z_j + log2 Vs - M) with M the running
+//    maximum of z_j + log2 Vs: fp16 weights are relative to the largest CONTRIBUTION, however far
+//    the pages' scales lie apart (rounding 2^-11 of each weight).  The sum of the softmax takes
+//    2^(z_j - M) in fp32.
+//  - The k index of the products runs through a lane's own bytes, so both operands come out of the
+//    swizzled tiles by 16-byte reads without bank conflicts; only the weights change places between
+//    lanes (movmatrix).
+
+constexpr int kTile = 32;       // keys of a stage
+constexpr int kPiece = 256;     // keys whose pages a warp holds at a time (at most 16 pages)
+constexpr int kAttnWarps = 8;
+constexpr int kStages = 3;
+
+template <int kD>
+struct AttnLayout {
+  static constexpr int kHalf = kTile * kD;                  // codes of K (or V) of a stage
+  static constexpr int kWarp = kStages * 2 * kHalf;
+  static constexpr int kBar = kAttnWarps * kWarp;           // after the rings
+  static constexpr int kPrefix = kBar + kAttnWarps * kStages * 8;
+  static constexpr int kMaxPrefix = 2048;                   // units are scanned in so many groups
+  static constexpr int kBytes = kPrefix + (kMaxPrefix + 1) * 4 + kAttnWarps * 4;
+  static constexpr int kAlloc = kBytes + 1024;
+};
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) { return __byte_perm(a, b, s); }
+
+// Codes in the low (high) two bytes of x as a pair of fp16.
+template <int kFmt>
+__device__ __forceinline__ uint32_t half2_lo(uint32_t x) {
+  uint32_t r;
+  if constexpr (kFmt == MOBA_CACHE_E4M3) {
+    asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;}" : "=r"(r) : "r"(x));
+  } else {
+    // byte + 128 as the low bits of 1024 + u, minus 1152
+    const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&(r = prmt(x, 0x64646464u, 0x4140))),
+                              __floats2half2_rn(1152.f, 1152.f));
+    r = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return r;
+}
+template <int kFmt>
+__device__ __forceinline__ uint32_t half2_hi(uint32_t x) {
+  uint32_t r;
+  if constexpr (kFmt == MOBA_CACHE_E4M3) {
+    asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;}" : "=r"(r) : "r"(x));
+  } else {
+    const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&(r = prmt(x, 0x64646464u, 0x4342))),
+                              __floats2half2_rn(1152.f, 1152.f));
+    r = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return r;
+}
+// Codes as they come, made ready for half2_lo / half2_hi.
+template <int kFmt>
+__device__ __forceinline__ uint32_t ready(uint32_t x) {
+  return kFmt == MOBA_CACHE_E4M3 ? x : x ^ 0x80808080u;
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// A run of at most kPiece keys of one unit (uniform over the warp).
+struct Piece {
+  int idx, unit;          // place in the work list
+  int s, gk, ht;
+  int32_t block;
+  int chunk;              // of the block
+  int key0, n, left;      // first key in the block, keys here, keys of the unit behind this piece
+  uint32_t slots[2];
+  bool begins;            // first piece of its unit
+};
+
+__device__ __forceinline__ void open_unit(const CacheGeom& g, const CacheDecodeWork& w, const int32_t* lens, Piece& p) {
+  const int HT = (g.G + 7) / 8;
+  p.ht = p.idx % HT;
+  const int sg = p.idx / HT;
+  p.gk = sg % g.Hkv;
+  p.s = sg / g.Hkv;
+  const int32_t len = cached_len(g, lens, p.s);
+  const int own = (len - 1) / g.bs, own_n = len - own * g.bs, own_chunks = (own_n + w.CK - 1) / w.CK;
+  int seg = 0, bn = own_n;
+  p.chunk = p.unit;
+  if (p.unit >= own_chunks) {
+    seg = 1 + (p.unit - own_chunks) / w.NC;
+    p.chunk = (p.unit - own_chunks) % w.NC;
+    bn = g.bs;
+  }
+  const int4 e = __ldg(reinterpret_cast<const int4*>(w.segs + (size_t)p.idx * w.max_segs + seg));
+  p.block = e.x;
+  p.slots[0] = (uint32_t)e.z;
+  p.slots[1] = (uint32_t)e.w;
+  p.key0 = p.chunk * w.CK;
+  const int n = min(w.CK, bn - p.key0);
+  p.n = min(n, kPiece);
+  p.left = n - p.n;
+  p.begins = true;
+}
+
 template <int kD, int kFmt>
-__global__ void __launch_bounds__(128)
-    cache_attn_kernel(CacheGeom g, const __nv_bfloat16* __restrict__ Q, const uint8_t* __restrict__ Kc,
-                      const uint8_t* __restrict__ Vc, const float* __restrict__ Ks, const float* __restrict__ Vs,
-                      const int32_t* __restrict__ lens, const int32_t* __restrict__ tables,
-                      const int32_t* __restrict__ sel, float* __restrict__ part_o, float* __restrict__ part_lse) {
-  constexpr int kDL = kD / 32;
-  __shared__ float red_o[4][kD], red_m[4], red_l[4];
-  const int slot = blockIdx.x, h = blockIdx.y, s = blockIdx.z, gk = h / g.G;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const size_t unit = ((size_t)s * g.Hq + h) * g.k + slot;
-  const int32_t b = __ldg(sel + unit);
-  if (b < 0) return;
-  const int32_t len = cached_len(g, lens, s), n = min(g.bs, len - b * g.bs);
-  float q[kDL], o[kDL], m = -INFINITY, l = 0.f;
+__global__ void __launch_bounds__(kAttnWarps * 32, 1)
+    cache_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, CacheGeom g,
+                      const __nv_bfloat16* __restrict__ Q, const float* __restrict__ Ks, const float* __restrict__ Vs,
+                      const int32_t* __restrict__ lens, const int32_t* __restrict__ tables, CacheDecodeWork w, int NI) {
+  using L = AttnLayout<kD>;
+  constexpr int kW = kD / 16;   // k steps of K Q^T = 16-row tiles of V^T
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, t = lane & 3;
+  uint8_t* ring = smem + warp * L::kWarp;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar) + warp * kStages;
+  int32_t* prefix = reinterpret_cast<int32_t*>(smem + L::kPrefix);
+  int32_t* wsum = prefix + L::kMaxPrefix + 1;
+
+  // ---- units before each group of `per` entries of the work list
+  const int per = (NI + L::kMaxPrefix - 1) / L::kMaxPrefix, groups = (NI + per - 1) / per;
+  constexpr int kEach = L::kMaxPrefix / (kAttnWarps * 32);
+  int32_t cnt[kEach], sum = 0;
 #pragma unroll
-  for (int x = 0; x < kDL; ++x) {
-    q[x] = __bfloat162float(Q[((size_t)s * g.Hq + h) * kD + lane * kDL + x]) * g.scale_log2;
-    o[x] = 0.f;
+  for (int x = 0; x < kEach; ++x) {
+    const int gr = threadIdx.x * kEach + x;
+    cnt[x] = 0;
+    if (gr < groups)
+      for (int y = gr * per; y < min(NI, (gr + 1) * per); ++y) cnt[x] += w.units[y];
+    sum += cnt[x];
   }
-  for (int j = warp; j < n; j += 4) {
-    const int pos = b * g.bs + j;
-    const int32_t page = __ldg(tables + (size_t)s * g.MP + pos / g.ps);
-    if (!page_ok(g, page)) {
-      if (lane == 0) atomicOr(g.err, kErrBadPage);
-      continue;
-    }
-    const size_t at = slab_offset(g, page, gk) + (size_t)(pos % g.ps) * kD + lane * kDL;
-    float z = 0.f, v[kDL];
+  int32_t inc = sum;
 #pragma unroll
-    for (int x = 0; x < kDL; x += 2) {
-      const float2 k2 = codes2_to_float2<kFmt>(*reinterpret_cast<const uint16_t*>(Kc + at + x));
-      const float2 v2 = codes2_to_float2<kFmt>(*reinterpret_cast<const uint16_t*>(Vc + at + x));
-      z = fmaf(q[x], k2.x, fmaf(q[x + 1], k2.y, z));
-      v[x] = v2.x;
-      v[x + 1] = v2.y;
-    }
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
-    z *= __ldg(Ks + (size_t)page * g.Hkv + gk);
-    const float vs = __ldg(Vs + (size_t)page * g.Hkv + gk);
-    const float m_new = fmaxf(m, z), alpha = m == m_new ? 1.f : exp2f(m - m_new), p = exp2f(z - m_new);
-    l = l * alpha + p;
-#pragma unroll
-    for (int x = 0; x < kDL; ++x) o[x] = fmaf(p * vs, v[x], o[x] * alpha);
-    m = m_new;
+  for (int off = 1; off < 32; off <<= 1) {
+    const int32_t o = __shfl_up_sync(0xffffffffu, inc, off);
+    if (lane >= off) inc += o;
   }
+  if (lane == 31) wsum[warp] = inc;
   if (lane == 0) {
-    red_m[warp] = m;
-    red_l[warp] = l;
+    for (int q = 0; q < kStages; ++q) mbar_init(&full[q], 1);
+    fence_mbar_init();
   }
-#pragma unroll
-  for (int x = 0; x < kDL; ++x) red_o[warp][lane * kDL + x] = o[x];
   __syncthreads();
-  if (threadIdx.x < kD) {
-    float M = -INFINITY, L = 0.f, acc = 0.f;
-    for (int w = 0; w < 4; ++w) M = fmaxf(M, red_m[w]);
-    for (int w = 0; w < 4; ++w) {
-      const float c = red_m[w] == -INFINITY && M != red_m[w] ? 0.f : exp2f(red_m[w] - M);
-      if (red_l[w] == 0.f) continue;  // no key of this warp
-      L = fmaf(red_l[w], c, L);
-      acc = fmaf(red_o[w][threadIdx.x], c, acc);
-    }
-    part_o[unit * kD + threadIdx.x] = L > 0.f || L != L ? acc / L : 0.f;
-    if (threadIdx.x == 0) part_lse[unit] = L > 0.f || L != L ? M + log2f(L) : -INFINITY;
+  int32_t before = inc - sum;
+  for (int q = 0; q < warp; ++q) before += wsum[q];
+#pragma unroll
+  for (int x = 0; x < kEach; ++x) {
+    prefix[threadIdx.x * kEach + x] = before;
+    before += cnt[x];
   }
+  if (threadIdx.x == kAttnWarps * 32 - 1) prefix[L::kMaxPrefix] = before;
+  __syncthreads();
+  const int32_t total = prefix[L::kMaxPrefix];
+  const int64_t W = (int64_t)gridDim.x * kAttnWarps, wid = (int64_t)blockIdx.x * kAttnWarps + warp;
+  int32_t todo = (int32_t)((wid + 1) * total / W) - (int32_t)(wid * total / W);  // units of this warp
+  if (todo == 0) return;
+
+  // ---- the first unit
+  Piece cur, nxt;
+  {
+    const int32_t u = (int32_t)(wid * total / W);
+    int lo = 0, hi = groups - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (prefix[mid] <= u) lo = mid; else hi = mid - 1;
+    }
+    cur.idx = lo * per;
+    cur.unit = u - prefix[lo];
+    for (int32_t c; cur.unit >= (c = w.units[cur.idx]);) cur.unit -= c, ++cur.idx;
+    open_unit(g, w, lens, cur);
+  }
+  // The piece after p; false behind the warp's last one.
+  auto advance = [&](const Piece& p, Piece& o) -> bool {
+    o = p;
+    if (p.left > 0) {
+      o.key0 = p.key0 + p.n;
+      o.n = min(p.left, kPiece);
+      o.left = p.left - o.n;
+      o.begins = false;
+      return true;
+    }
+    if (--todo == 0) return false;
+    ++o.unit;
+    while (o.unit >= w.units[o.idx]) o.unit = 0, ++o.idx;
+    open_unit(g, w, lens, o);
+    return true;
+  };
+  // Page of the lane-th run of ps keys (-1: none; bad ones are reported) and the pages' scales.
+  auto pages_of = [&](const Piece& p) -> int32_t {
+    int32_t page = -1;
+    if (lane * g.ps < p.n) {
+      page = __ldg(tables + (size_t)p.s * g.MP + (p.block * g.bs + p.key0) / g.ps + lane);
+      if (!page_ok(g, page)) {
+        atomicOr(g.err, kErrBadPage);
+        page = -1;
+      }
+    }
+    return page;
+  };
+  const int box = min(g.ps, kTile);
+  int wr = 0;  // stage that the next copy goes to
+  auto issue = [&](const Piece& p, int32_t page, int tile) {
+    uint8_t* dst = ring + wr * 2 * L::kHalf;
+    int32_t pg[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int key = tile * kTile + x * box;
+      pg[x] = __shfl_sync(0xffffffffu, page, (key / g.ps) & 31);
+      if (x * box >= kTile || key >= p.n) pg[x] = -1;
+    }
+    if (lane == 0) {
+      const uint32_t bytes = (uint32_t)((pg[0] >= 0) + (pg[1] >= 0)) * 2u * box * kD;
+      if (bytes) mbar_expect_tx(&full[wr], bytes); else mbar_arrive(&full[wr]);
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (pg[x] >= 0) {
+          const int row = (p.key0 + tile * kTile + x * box) % g.ps, slab = pg[x] * g.Hkv + p.gk;
+          tma_load_3d(dst + x * box * kD, &tmK, &full[wr], 0, row, slab);
+          tma_load_3d(dst + L::kHalf + x * box * kD, &tmV, &full[wr], 0, row, slab);
+        }
+    }
+    if (++wr == kStages) wr = 0;
+  };
+  auto tiles_of = [](const Piece& p) { return (p.n + kTile - 1) / kTile; };
+
+  int32_t page_c = pages_of(cur), page_n = -1;
+  int issued_c = 0, issued_n = 0, flying = 0;
+  for (; issued_c < min(tiles_of(cur), kStages); ++issued_c, ++flying) issue(cur, page_c, issued_c);
+  bool more = advance(cur, nxt), ok = true;
+  if (more) page_n = pages_of(nxt);
+  float ks = page_c >= 0 ? __ldg(Ks + (size_t)page_c * g.Hkv + cur.gk) : 0.f;
+  float vs = page_c >= 0 ? __ldg(Vs + (size_t)page_c * g.Hkv + cur.gk) : 1.f;
+  int rd = 0;
+  uint32_t parity = 0;
+
+  uint32_t qb[kW][2];
+  float sf[2];                  // of heads 2t, 2t + 1: softmax scale over Q's power of two, log2 units
+  int q_idx = -1;
+  float o[kW][4], m[2], l[2];
+
+  while (true) {
+    if (cur.begins) {
+      if (q_idx != cur.idx) {
+        // Q of head gq, dimensions [t * kD / 4, (t + 1) * kD / 4), as the products' second operand
+        q_idx = cur.idx;
+        const int h = cur.ht * 8 + gq;
+        const bool live = h < g.G;
+        const uint2* src = reinterpret_cast<const uint2*>(Q + ((size_t)cur.s * g.Hq + (size_t)cur.gk * g.G + h) * kD) + t * kW;
+        uint2 raw[kW];
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < kW; ++j) {
+          raw[j] = live ? __ldg(src + j) : make_uint2(0, 0);
+          top = max(max(top, max(raw[j].x & 0x7fffu, (raw[j].x >> 16) & 0x7fffu)),
+                    max(raw[j].y & 0x7fffu, (raw[j].y >> 16) & 0x7fffu));
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // largest element to [2^14, 2^15); an infinity or NaN stays what it is
+        const int ex = (int)(top >> 7), sh = ex == 255 ? 0 : min(141 - ex, 126);
+        const float f = __int_as_float((127 + sh) << 23);
+#pragma unroll
+        for (int j = 0; j < kW; ++j) {
+          const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[j].x));
+          const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[j].y));
+          qb[j][0] = pack_half2(lo.x * f, lo.y * f);
+          qb[j][1] = pack_half2(hi.x * f, hi.y * f);
+        }
+        const float mine = g.scale_log2 * __int_as_float((127 - sh) << 23);
+        sf[0] = __shfl_sync(0xffffffffu, mine, 8 * t);      // a lane of head 2t
+        sf[1] = __shfl_sync(0xffffffffu, mine, 8 * t + 4);
+      }
+#pragma unroll
+      for (int j = 0; j < kW; ++j)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[j][x] = 0.f;
+      m[0] = m[1] = -INFINITY;
+      l[0] = l[1] = 0.f;
+    }
+    const float lvs = log2f(vs);
+    const int tiles = tiles_of(cur);
+    for (int tile = 0; tile < tiles; ++tile) {
+      ok = mbar_wait_warp(&full[rd], parity, g.err);
+      if (!ok) break;
+      const uint8_t* kst = ring + rd * 2 * L::kHalf;
+      const uint8_t* vst = kst + L::kHalf;
+      float z[2][4];
+      // ---- S = K Q^T: keys gq and gq + 8 of each 16, heads 2t and 2t + 1
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        uint32_t kw[2][kW];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int r = mt * 16 + x * 8 + gq;
+          if constexpr (kD == 128) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const uint4 v = *reinterpret_cast<const uint4*>(kst + r * 128 + (((2 * t + c) ^ (r & 7)) << 4));
+              kw[x][4 * c] = v.x, kw[x][4 * c + 1] = v.y, kw[x][4 * c + 2] = v.z, kw[x][4 * c + 3] = v.w;
+            }
+          } else {
+            const uint4 v = *reinterpret_cast<const uint4*>(kst + r * 64 + ((t ^ ((r >> 1) & 3)) << 4));
+            kw[x][0] = v.x, kw[x][1] = v.y, kw[x][2] = v.z, kw[x][3] = v.w;
+          }
+        }
+        float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < kW; ++j) {
+          const uint32_t a = ready<kFmt>(kw[0][j]), b = ready<kFmt>(kw[1][j]);
+          mma_f16(j & 1 ? c1 : c0, half2_lo<kFmt>(a), half2_lo<kFmt>(b), half2_hi<kFmt>(a), half2_hi<kFmt>(b), qb[j][0],
+                  qb[j][1]);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) z[mt][x] = c0[x] + c1[x];
+      }
+      // ---- online softmax
+      int live[2];     // keys of each 16 that count
+      float zw[2][4];  // with the value scale
+      float mx0 = m[0], mx1 = m[1];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        const int key = tile * kTile + mt * 16, pi = (key / g.ps) & 31;
+        const float k1 = __shfl_sync(0xffffffffu, ks, pi), lv = __shfl_sync(0xffffffffu, lvs, pi);
+        const int32_t pg = __shfl_sync(0xffffffffu, page_c, pi);
+        live[mt] = pg >= 0 ? min(16, cur.n - key) : 0;
+        z[mt][0] *= k1 * sf[0];
+        z[mt][1] *= k1 * sf[1];
+        z[mt][2] *= k1 * sf[0];
+        z[mt][3] *= k1 * sf[1];
+        if (live[mt] < 16) {
+          if (gq >= live[mt]) z[mt][0] = z[mt][1] = -INFINITY;
+          if (gq + 8 >= live[mt]) z[mt][2] = z[mt][3] = -INFINITY;
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) zw[mt][x] = z[mt][x] + lv;
+        mx0 = max3(mx0, zw[mt][0], zw[mt][2]);
+        mx1 = max3(mx1, zw[mt][1], zw[mt][3]);
+      }
+#pragma unroll
+      for (int off = 4; off <= 16; off <<= 1) {
+        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
+      }
+      const float b0 = mx0 == -INFINITY ? 0.f : mx0, b1 = mx1 == -INFINITY ? 0.f : mx1;
+      if (__any_sync(0xffffffffu, mx0 != m[0] || mx1 != m[1])) {
+        const float a0 = ex2(m[0] - b0), a1 = ex2(m[1] - b1);
+        l[0] *= a0;
+        l[1] *= a1;
+#pragma unroll
+        for (int j = 0; j < kW; ++j) {
+          o[j][0] *= a0;
+          o[j][1] *= a1;
+          o[j][2] *= a0;
+          o[j][3] *= a1;
+        }
+        m[0] = mx0;
+        m[1] = mx1;
+      }
+      // ---- O += V^T P: dimensions of group gq, heads 2t and 2t + 1
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        l[0] += ex2(z[mt][0] - b0) + ex2(z[mt][2] - b0);
+        l[1] += ex2(z[mt][1] - b1) + ex2(z[mt][3] - b1);
+        const uint32_t p0 = transpose8(pack_half2(ex2(zw[mt][0] - b0), ex2(zw[mt][1] - b1)));
+        const uint32_t p1 = transpose8(pack_half2(ex2(zw[mt][2] - b0), ex2(zw[mt][3] - b1)));
+        uint32_t v[4][kW / 2];  // keys 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int kk = 2 * t + (x & 1) + 8 * (x >> 1), r = mt * 16 + kk;
+          if constexpr (kD == 128) {
+            const uint4 u = *reinterpret_cast<const uint4*>(vst + r * 128 + ((gq ^ (r & 7)) << 4));
+            v[x][0] = u.x, v[x][1] = u.y, v[x][2] = u.z, v[x][3] = u.w;
+          } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(vst + r * 64 + (((gq >> 1) ^ ((r >> 1) & 3)) << 4) + (gq & 1) * 8);
+            v[x][0] = u.x, v[x][1] = u.y;
+          }
+          if (live[mt] < 16 && kk >= live[mt])  // whatever stands there must not meet a weight of 0
+#pragma unroll
+            for (int j = 0; j < kW / 2; ++j) v[x][j] = 0;
+        }
+#pragma unroll
+        for (int j = 0; j < kW / 2; ++j) {
+          const uint32_t a = ready<kFmt>(v[0][j]), b = ready<kFmt>(v[1][j]), c = ready<kFmt>(v[2][j]), d = ready<kFmt>(v[3][j]);
+          const uint32_t x0 = prmt(a, b, 0x5140), x1 = prmt(a, b, 0x7362), y0 = prmt(c, d, 0x5140), y1 = prmt(c, d, 0x7362);
+          mma_f16(o[2 * j], half2_lo<kFmt>(x0), half2_hi<kFmt>(x0), half2_lo<kFmt>(y0), half2_hi<kFmt>(y0), p0, p1);
+          mma_f16(o[2 * j + 1], half2_lo<kFmt>(x1), half2_hi<kFmt>(x1), half2_lo<kFmt>(y1), half2_hi<kFmt>(y1), p0, p1);
+        }
+      }
+      __syncwarp();  // the stage is read
+      if (++rd == kStages) rd = 0, parity ^= 1;
+      --flying;
+      if (issued_c < tiles) issue(cur, page_c, issued_c++), ++flying;
+      else if (more && issued_n < tiles_of(nxt)) issue(nxt, page_n, issued_n++), ++flying;
+    }
+    if (!ok) break;
+    if (cur.left == 0) {
+      // ---- partial result of the unit
+      float ls[2] = {l[0], l[1]};
+#pragma unroll
+      for (int off = 4; off <= 16; off <<= 1) {
+        ls[0] += __shfl_xor_sync(0xffffffffu, ls[0], off);
+        ls[1] += __shfl_xor_sync(0xffffffffu, ls[1], off);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int h = 2 * t + e;
+        const uint32_t slot = ((t < 2 ? cur.slots[0] : cur.slots[1]) >> 8 * (h & 3)) & 0xffu;
+        if (slot != 0xffu) {
+          const size_t row = (size_t)cur.s * g.Hq + (size_t)cur.gk * g.G + cur.ht * 8 + h;
+          const size_t part = (row * g.k + slot) * w.NC + cur.chunk;
+          float4* dst = reinterpret_cast<float4*>(w.part_o + part * kD + gq * (kD / 8));
+#pragma unroll
+          for (int j = 0; j < kW; j += 2) dst[j / 2] = make_float4(o[j][e], o[j][2 + e], o[j + 1][e], o[j + 1][2 + e]);
+          if (gq == 0) w.part_ml[part] = make_float2(m[e], ls[e]);
+        }
+      }
+    }
+    if (!more) break;
+    cur = nxt;
+    page_c = page_n;
+    issued_c = issued_n;
+    issued_n = 0;
+    ks = page_c >= 0 ? __ldg(Ks + (size_t)page_c * g.Hkv + cur.gk) : 0.f;
+    vs = page_c >= 0 ? __ldg(Vs + (size_t)page_c * g.Hkv + cur.gk) : 1.f;
+    for (; flying < kStages && issued_c < tiles_of(cur); ++flying) issue(cur, page_c, issued_c++);
+    more = advance(cur, nxt);
+    page_n = more ? pages_of(nxt) : -1;
+  }
+  if (!ok)  // a wait gave up: leave no copy behind
+    for (; flying > 0; --flying) {
+      mbar_wait_warp(&full[rd], parity, g.err);
+      if (++rd == kStages) rd = 0, parity ^= 1;
+    }
 }
 
-// The slots of a (request, head) merged by online softmax; part_lse in log2 units.
+// The chunks of a (request, head), one warp each row, merged by online softmax (log2 units).
 template <int kD>
 __global__ void __launch_bounds__(128)
-    cache_merge_kernel(CacheGeom g, const int32_t* __restrict__ sel, const float* __restrict__ part_o,
-                       const float* __restrict__ part_lse, __nv_bfloat16* __restrict__ O, float* __restrict__ LSE) {
+    cache_merge_kernel(CacheGeom g, const int32_t* __restrict__ lens, const int32_t* __restrict__ sel,
+                       CacheDecodeWork w, __nv_bfloat16* __restrict__ O, float* __restrict__ LSE) {
   constexpr int kDL = kD / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const size_t row = (size_t)blockIdx.x * 4 + warp;
   if (row >= (size_t)g.B * g.Hq) return;
-  float M = -INFINITY, L = 0.f, acc[kDL];
+  const int32_t len = cached_len(g, lens, (int)(row / g.Hq));
+  const int own_n = len > 0 ? len - (len - 1) / g.bs * g.bs : 0, own_chunks = (own_n + w.CK - 1) / w.CK;
+  const int32_t my = lane < g.k ? __ldg(sel + row * g.k + lane) : -1;
+  const int slots = __popc(__ballot_sync(0xffffffffu, my >= 0));  // filled from the front
+  const int n = slots ? own_chunks + (slots - 1) * w.NC : 0;
+  const float2* ml = w.part_ml + row * g.k * w.NC;
+  const float* po = w.part_o + row * g.k * w.NC * kD + lane * kDL;
+  auto at = [&](int x) { return x < own_chunks ? x : w.NC + (x - own_chunks); };
+  float M = -INFINITY;
+  for (int x = lane; x < n; x += 32) M = fmaxf(M, ml[at(x)].x);
 #pragma unroll
-  for (int x = 0; x < kDL; ++x) acc[x] = 0.f;
-  for (int q = 0; q < g.k; ++q)
-    if (__ldg(sel + row * g.k + q) >= 0) M = fmaxf(M, __ldg(part_lse + row * g.k + q));
-  for (int q = 0; q < g.k; ++q) {
-    if (__ldg(sel + row * g.k + q) < 0) continue;
-    const float t = __ldg(part_lse + row * g.k + q);
-    if (t == -INFINITY) continue;  // no key in this block
-    const float w = exp2f(t - M);
-    L += w;
+  for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  const float base = M == -INFINITY ? 0.f : M;
+  float L = 0.f, acc[kDL];
 #pragma unroll
-    for (int x = 0; x < kDL; ++x) acc[x] = fmaf(w, __ldg(part_o + (row * g.k + q) * kD + lane * kDL + x), acc[x]);
+  for (int d = 0; d < kDL; ++d) acc[d] = 0.f;
+  for (int x0 = 0; x0 < n; x0 += 32) {
+    float wt = 0.f;
+    if (x0 + lane < n) {
+      const float2 v = ml[at(x0 + lane)];
+      wt = ex2(v.x - base);
+      L = fmaf(v.y, wt, L);
+    }
+    const int c = min(32, n - x0);
+#pragma unroll 8
+    for (int x = 0; x < c; ++x) {
+      const float wx = __shfl_sync(0xffffffffu, wt, x);
+      const float* src = po + (size_t)at(x0 + x) * kD;
+      if constexpr (kDL == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(src);
+        acc[0] = fmaf(wx, f.x, acc[0]);
+        acc[1] = fmaf(wx, f.y, acc[1]);
+        acc[2] = fmaf(wx, f.z, acc[2]);
+        acc[3] = fmaf(wx, f.w, acc[3]);
+      } else {
+        const float2 f = *reinterpret_cast<const float2*>(src);
+        acc[0] = fmaf(wx, f.x, acc[0]);
+        acc[1] = fmaf(wx, f.y, acc[1]);
+      }
+    }
   }
-  const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
-  for (int x = 0; x < kDL; x += 2)
-    *reinterpret_cast<__nv_bfloat162*>(O + row * kD + lane * kDL + x) = __floats2bfloat162_rn(acc[x] * inv, acc[x + 1] * inv);
+  for (int off = 16; off >= 1; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+  const float inv = L == 0.f ? 0.f : 1.f / L;  // 0: no key at all
+#pragma unroll
+  for (int d = 0; d < kDL; d += 2)
+    *reinterpret_cast<__nv_bfloat162*>(O + row * kD + lane * kDL + d) = __floats2bfloat162_rn(acc[d] * inv, acc[d + 1] * inv);
   if (lane == 0) LSE[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2C;
+}
+
+// ---------------------------------------------------------------------------------- launch
+
+// Codes [P * Hkv, ps, D] as dims (d, row, slab); boxes of D x min(ps, kTile) x 1, swizzled over the
+// whole row (128 or 64 bytes).
+cudaError_t make_codes_map(CUtensorMap* m, const void* base, const CacheGeom& g) {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  if (!fn) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    if (!fn) return cudaErrorNotSupported;
+  }
+  const cuuint64_t dims[3] = {(cuuint64_t)g.D, (cuuint64_t)g.ps, (cuuint64_t)g.P * g.Hkv};
+  const cuuint64_t strides[2] = {(cuuint64_t)g.D, (cuuint64_t)g.D * g.ps};
+  const cuuint32_t box[3] = {(cuuint32_t)g.D, (cuuint32_t)(g.ps < kTile ? g.ps : kTile), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        g.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int kD, int kH>
+cudaError_t launch_gate(const CacheGeom& g, const __nv_bfloat16* Q, const float* Kbar, const int32_t* lens,
+                        int32_t* sel, const CacheDecodeWork& w, cudaStream_t st) {
+  // CTAs of a cluster share the candidates: 8 warps take 32 / kH blocks each at a time
+  int c = 1;
+  while (c < 8 && g.k > 1 && c * kGateWarps * (32 / kH) < g.MB - 1) c *= 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)c, (unsigned)g.Hkv, (unsigned)g.B);
+  cfg.blockDim = dim3(kGateWarps * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)c;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_gate_kernel<kD, kH>, g, Q, Kbar, lens, sel, w);
 }
 
 template <int kD, int kFmt>
 cudaError_t launch_decode_t(const CacheGeom& g, const __nv_bfloat16* Q, const uint8_t* Kc, const uint8_t* Vc,
                             const float* Ks, const float* Vs, const float* Kbar, const int32_t* lens,
                             const int32_t* tables, int32_t* sel, const CacheDecodeWork& w, __nv_bfloat16* O,
-                            float* LSE, cudaStream_t st) {
-  cache_gate_kernel<kD><<<dim3((unsigned)g.Hkv, (unsigned)g.B), 256, 0, st>>>(g, Q, Kbar, lens, w.score, sel);
-  cudaError_t e = cudaGetLastError();
+                            float* LSE, int sms, cudaStream_t st) {
+  cudaError_t e = g.G == 1   ? launch_gate<kD, 1>(g, Q, Kbar, lens, sel, w, st)
+                  : g.G == 2 ? launch_gate<kD, 2>(g, Q, Kbar, lens, sel, w, st)
+                             : launch_gate<kD, 4>(g, Q, Kbar, lens, sel, w, st);
   if (e != cudaSuccess) return e;
-  cache_attn_kernel<kD, kFmt><<<dim3((unsigned)g.k, (unsigned)g.Hq, (unsigned)g.B), 128, 0, st>>>(
-      g, Q, Kc, Vc, Ks, Vs, lens, tables, sel, w.part_o, w.part_lse);
+  CUtensorMap tk, tv;
+  if ((e = make_codes_map(&tk, Kc, g)) != cudaSuccess) return e;
+  if ((e = make_codes_map(&tv, Vc, g)) != cudaSuccess) return e;
+  auto attn = cache_attn_kernel<kD, kFmt>;
+  if ((e = cudaFuncSetAttribute(attn, cudaFuncAttributeMaxDynamicSharedMemorySize, AttnLayout<kD>::kAlloc)) != cudaSuccess)
+    return e;
+  const int NI = g.B * g.Hkv * ((g.G + 7) / 8);
+  attn<<<sms, kAttnWarps * 32, AttnLayout<kD>::kAlloc, st>>>(tk, tv, g, Q, Ks, Vs, lens, tables, w, NI);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const size_t rows = (size_t)g.B * g.Hq;
-  cache_merge_kernel<kD><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(g, sel, w.part_o, w.part_lse, O, LSE);
+  cache_merge_kernel<kD><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(g, lens, sel, w, O, LSE);
   return cudaGetLastError();
 }
 
 }  // namespace
 
+// Keys of a unit.  Long chunks write fewer partial rows, short ones spread a small problem over the
+// GPU: the longest that leaves every warp two units if all heads of a group agree, at least 128.
+// A power of two, so that the pieces of every unit start on a page.
+int cache_chunk_keys(const CacheGeom& g) {
+  const int64_t rows = (int64_t)g.B * g.Hkv * ((g.G + 7) / 8) * g.k;
+  int ck = 8192;
+  while (ck > 128 && (ck / 2 >= g.bs || rows * ((g.bs + ck - 1) / ck) < 2 * 148 * kAttnWarps)) ck /= 2;
+  return ck;
+}
+
 cudaError_t launch_cache_decode(const CacheGeom& g, const __nv_bfloat16* Q, const uint8_t* Kc, const uint8_t* Vc,
                                 const float* Ks, const float* Vs, const float* Kbar, const int32_t* lens,
                                 const int32_t* tables, int32_t* sel, const CacheDecodeWork& w, __nv_bfloat16* O,
                                 float* LSE, cudaStream_t st) {
-  auto go = [&](auto fn) { return fn(g, Q, Kc, Vc, Ks, Vs, Kbar, lens, tables, sel, w, O, LSE, st); };
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  auto go = [&](auto fn) { return fn(g, Q, Kc, Vc, Ks, Vs, Kbar, lens, tables, sel, w, O, LSE, sms, st); };
   if (g.D == 64)
     return g.fmt == MOBA_CACHE_E4M3 ? go(launch_decode_t<64, MOBA_CACHE_E4M3>) : go(launch_decode_t<64, MOBA_CACHE_INT8>);
   return g.fmt == MOBA_CACHE_E4M3 ? go(launch_decode_t<128, MOBA_CACHE_E4M3>) : go(launch_decode_t<128, MOBA_CACHE_INT8>);
