@@ -5,195 +5,416 @@
 //   scale = off > 0 ? max(old scale, t) : t             (qmax: 448 for e4m3, 127 for int8)
 //   code  = rn(x / scale), clamped;   older codes, when the scale grew: rn(code * old / scale).
 // Scales are kept to 8 significant bits, as bf16 values have: a quotient of two such numbers is
-// either exactly half-way between two codes or at least 2^-17 (relative) away from there, so the
-// fp32 quotient never lands on the wrong side and codes equal those of the exact formula.
+// either exactly half-way between two codes or at least 2^-17 (relative) away from there, so fp32
+// arithmetic can place every code where the exact formula places it.
 //
 // A MoBA block whose last token this call writes gets its pooled key: the mean of the block's
-// stored (dequantised) keys, read back from the pages; the gate then ranks what attention sees.
+// stored (dequantised) keys, so that the gate ranks what attention sees.
 //
 // Bound by HBM for prompts (bf16 in, codes out: 6 bytes for each element of K and V together), by
-// latency for single tokens.  One CTA per (request, KV head, K or V) takes the request's touched
-// pages one after the other.
-#include "moba.h"
+// latency for single tokens.  Two forms of one body:
+//   cache_append_kernel : a CTA for each (request, KV head, K or V) takes the request's touched
+//                         pages one after the other: one launch of few CTAs for decode steps.
+//   cache_prompt_kernel : a cluster of up to 8 CTAs for each (touched MoBA block, KV head, K or V);
+//                         its CTAs share the block's pages and add up the pooled key on the way.
 #include <float.h>
 
 #include "cache.cuh"
+#include "sm100.cuh"
 
 namespace moba {
 namespace {
 
-constexpr int kAppThreads = 256;
+constexpr int kAppThreads = 256, kAppWarps = kAppThreads / 32;
 constexpr float kTiny = 0x1p-96f;  // keeps scales and quotients far from the subnormal range
+constexpr uint32_t kInfBits = 0x7f80;  // magnitude bits of a bf16 infinity; NaN lies above
 
-// max over the block (every thread gets it); red holds one value a warp.
-__device__ __forceinline__ float block_max(float x, float* red) {
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-  __syncthreads();
-  x = red[0];
-#pragma unroll
-  for (int w = 1; w < kAppThreads / 32; ++w) x = fmaxf(x, red[w]);
-  return x;
+template <int kFmt>
+__device__ constexpr float qmax_of() {
+  return kFmt == MOBA_CACHE_E4M3 ? 448.f : 127.f;
 }
 
 // Least number of 8 significant bits that takes magnitude a to the largest code.
 template <int kFmt>
 __device__ __forceinline__ float scale_for(float a) {
-  constexpr float qmax = kFmt == MOBA_CACHE_E4M3 ? 448.f : 127.f;
   a = fmaxf(a, kTiny);
-  const uint32_t down = __float_as_uint(__fdiv_rn(a, qmax)) & 0xffff0000u;
-  // 8 bits times 7 bits: the product is exact
-  return __uint_as_float(__uint_as_float(down) * qmax < a ? down + 0x10000u : down);
+  const uint32_t down = __float_as_uint(__fdiv_rn(a, qmax_of<kFmt>())) & 0xffff0000u;
+  // 8 bits times at most 7 bits: the product is exact
+  return __uint_as_float(__uint_as_float(down) * qmax_of<kFmt>() < a ? down + 0x10000u : down);
 }
 
-__device__ __forceinline__ float finite_abs(float x) {
-  const float a = fabsf(x);
-  return a <= FLT_MAX ? a : 0.f;  // NaN fails the comparison too
+// x / s for x and s of 8 significant bits, given inv = rn(1 / s), close enough to be rounded to a
+// code: x * inv is within 2^-23 of the quotient (two roundings of 2^-24); rounding it to 20 bits
+// gives back a quotient that lies half-way between codes (at most 9 bits) exactly, and moves any
+// other by less than the 2^-17 that separate it from there.  Finite x only.  Three operations where
+// a division takes about ten.
+__device__ __forceinline__ float snapped_quotient(float x, float inv) {
+  return __uint_as_float((__float_as_uint(x * inv) + 8u) & ~15u);
 }
 
-// Rows [0, nr) of src (token stride `stride` elements) into rows [off, off + nr) of a slab.
-template <int kD, int kFmt>
-__device__ __forceinline__ void quantise_rows(const __nv_bfloat16* __restrict__ src, int64_t stride, int nr, int off,
-                                              uint8_t* slab, float* scale_ptr, float* red) {
-  constexpr int kVec = kD / 8;                        // 16-byte vectors of a row
-  constexpr int kIt = 128 * kVec / kAppThreads;       // for the largest page
+// Four values as codes.  kClean: no infinity or NaN among them, and magnitudes up to the largest code.
+template <int kFmt, bool kClean>
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+  if constexpr (kFmt == MOBA_CACHE_INT8 && kClean) {
+    // adding 1.5 * 2^23 rounds to an integer, ties to even, and leaves it in the low byte
+    constexpr float kMagic = 12582912.f;
+    const uint32_t lo = __byte_perm(__float_as_uint(a + kMagic), __float_as_uint(b + kMagic), 0x0040);
+    const uint32_t hi = __byte_perm(__float_as_uint(c + kMagic), __float_as_uint(d + kMagic), 0x0040);
+    return __byte_perm(lo, hi, 0x5410);
+  } else {
+    return float2_to_codes2<kFmt>(a, b) | float2_to_codes2<kFmt>(c, d) << 16;
+  }
+}
+
+__device__ __forceinline__ float2 bf16x2_to_float2(uint32_t x) {
+  return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+}
+
+// Eight values over the scale as codes; a page with an infinity or NaN (not kClean) is divided plainly.
+template <int kFmt, bool kClean>
+__device__ __forceinline__ uint2 quantise8(const uint4& x, float scale, float inv) {
+  auto q = [&](float v) { return kClean ? snapped_quotient(v, inv) : __fdiv_rn(v, scale); };
+  const float2 a = bf16x2_to_float2(x.x), b = bf16x2_to_float2(x.y), c = bf16x2_to_float2(x.z), d = bf16x2_to_float2(x.w);
+  return make_uint2(codes4<kFmt, kClean>(q(a.x), q(a.y), q(b.x), q(b.y)),
+                    codes4<kFmt, kClean>(q(c.x), q(c.y), q(d.x), q(d.y)));
+}
+
+// Eight codes added to eight sums.
+template <int kFmt>
+__device__ __forceinline__ void add_codes8(float (&sum)[8], const uint2& c) {
+  const uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const float2 lo = codes2_to_float2<kFmt>(w[e]), hi = codes2_to_float2<kFmt>(w[e] >> 16);
+    sum[4 * e] += lo.x;
+    sum[4 * e + 1] += lo.y;
+    sum[4 * e + 2] += hi.x;
+    sum[4 * e + 3] += hi.y;
+  }
+}
+
+// Largest magnitude (bf16 bits) over the block; red holds one value a warp and is used by one call
+// out of two, so that one barrier a call is enough.
+__device__ __forceinline__ uint32_t block_max(uint32_t x, uint32_t* red) {
+  x = __reduce_max_sync(0xffffffffu, x);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+  __syncthreads();
+  x = red[0];
+#pragma unroll
+  for (int w = 1; w < kAppWarps; ++w) x = max(x, red[w]);
+  return x;
+}
+
+// Shared memory of a CTA.
+template <int kD>
+struct AppendSmem {
+  uint32_t red[2][kAppWarps];
+  float pool[kAppWarps][kD];
+  float part[kD];  // this CTA's share of a pooled key
+};
+
+// The rows of one (page, KV head): thread holds vector v (8 columns) of rows r + it * kRows.
+template <int kD, int kFmt, int kIt>
+struct PageRows {
+  static constexpr int kVec = kD / 8, kRows = kAppThreads / kVec;
   uint4 x[kIt];
-  float a = 0.f;
+
+  __device__ __forceinline__ void load(const __nv_bfloat16* __restrict__ src, int64_t stride, int nr) {
+    const int v = threadIdx.x % kVec, r = threadIdx.x / kVec;
 #pragma unroll
-  for (int it = 0; it < kIt; ++it) {
-    const int i = it * kAppThreads + (int)threadIdx.x, r = i / kVec, v = i % kVec;
-    if (r < nr) {
-      x[it] = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)r * stride) + v);
-      const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&x[it]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = __bfloat1622float2(h[e]);
-        a = fmaxf(a, fmaxf(finite_abs(f.x), finite_abs(f.y)));
-      }
+    for (int it = 0; it < kIt; ++it) {
+      x[it] = make_uint4(0, 0, 0, 0);
+      if (r + it * kRows < nr)
+        x[it] = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)(r + it * kRows) * stride) + v);
     }
   }
-  a = block_max(a, red);
-  const float old = off > 0 ? *scale_ptr : 0.f;
-  float scale = scale_for<kFmt>(a);
-  if (off > 0 && old > scale) scale = old;
-  __syncthreads();  // every thread has read the old scale
-  if (threadIdx.x == 0) *scale_ptr = scale;
-  if (off > 0 && old < scale) {
-    uint2* rows = reinterpret_cast<uint2*>(slab);
-    for (int i = threadIdx.x; i < off * kVec; i += kAppThreads) {
-      const uint2 c = rows[i];
-      uint32_t in[2] = {c.x, c.y}, out[2];
+
+  // Into rows [off, off + nr) of the slab.  kPool: sum += codes of the new rows.  Returns the scale.
+  template <bool kPool>
+  __device__ __forceinline__ float store(int nr, int off, uint8_t* slab, float* scale_ptr, uint32_t (*red)[kAppWarps],
+                                         int& turn, float (&sum)[8]) {
+    const int v = threadIdx.x % kVec, r = threadIdx.x / kVec;
+    uint32_t big2 = 0;  // two magnitudes side by side
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float2 lo = codes2_to_float2<kFmt>(in[e]), hi = codes2_to_float2<kFmt>(in[e] >> 16);
-        out[e] = float2_to_codes2<kFmt>(__fdiv_rn(lo.x * old, scale), __fdiv_rn(lo.y * old, scale)) |
-                 float2_to_codes2<kFmt>(__fdiv_rn(hi.x * old, scale), __fdiv_rn(hi.y * old, scale)) << 16;
-      }
-      rows[i] = make_uint2(out[0], out[1]);
+    for (int it = 0; it < kIt; ++it) {
+      const uint32_t a = __vmaxu2(x[it].x & 0x7fff7fffu, x[it].y & 0x7fff7fffu);
+      const uint32_t b = __vmaxu2(x[it].z & 0x7fff7fffu, x[it].w & 0x7fff7fffu);
+      big2 = __vmaxu2(big2, __vmaxu2(a, b));
     }
-  }
+    uint32_t big = block_max(max(big2 & 0xffffu, big2 >> 16), red[turn ^= 1]);
+    const bool clean = big < kInfBits;
+    if (!clean) {  // the scale is that of the finite values
+      big = 0;
 #pragma unroll
-  for (int it = 0; it < kIt; ++it) {
-    const int i = it * kAppThreads + (int)threadIdx.x, r = i / kVec, v = i % kVec;
-    if (r < nr) {
-      const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&x[it]);
-      uint32_t out[2];
+      for (int it = 0; it < kIt; ++it) {
+        const uint32_t w[4] = {x[it].x, x[it].y, x[it].z, x[it].w};
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float2 lo = __bfloat1622float2(h[2 * e]), hi = __bfloat1622float2(h[2 * e + 1]);
-        out[e] = float2_to_codes2<kFmt>(__fdiv_rn(lo.x, scale), __fdiv_rn(lo.y, scale)) |
-                 float2_to_codes2<kFmt>(__fdiv_rn(hi.x, scale), __fdiv_rn(hi.y, scale)) << 16;
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t lo = w[e] & 0x7fffu, hi = (w[e] >> 16) & 0x7fffu;
+          big = max(big, max(lo < kInfBits ? lo : 0u, hi < kInfBits ? hi : 0u));
+        }
       }
-      reinterpret_cast<uint2*>(slab + (size_t)(off + r) * kD)[v] = make_uint2(out[0], out[1]);
+      big = block_max(big, red[turn ^= 1]);
     }
+    float scale = scale_for<kFmt>(__uint_as_float(big << 16));
+    if (off > 0) {
+      const float old = *scale_ptr;
+      if (old > scale) scale = old;
+      __syncthreads();  // every thread has read the old scale
+      if (old < scale) {
+        uint2* rows = reinterpret_cast<uint2*>(slab);
+        for (int i = threadIdx.x; i < off * kVec; i += kAppThreads) {
+          const uint2 c = rows[i];
+          const uint32_t in[2] = {c.x, c.y};
+          uint32_t out[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 lo = codes2_to_float2<kFmt>(in[e]), hi = codes2_to_float2<kFmt>(in[e] >> 16);
+            // the product is exact (at most 15 bits), the quotient as close as one of 8-bit numbers needs
+            out[e] = codes4<kFmt, false>(__fdiv_rn(lo.x * old, scale), __fdiv_rn(lo.y * old, scale),
+                                         __fdiv_rn(hi.x * old, scale), __fdiv_rn(hi.y * old, scale));
+          }
+          rows[i] = make_uint2(out[0], out[1]);
+        }
+      }
+    }
+    if (threadIdx.x == 0) *scale_ptr = scale;
+    const float inv = __frcp_rn(scale);
+#pragma unroll
+    for (int it = 0; it < kIt; ++it)
+      if (r + it * kRows < nr) {
+        const uint2 c = clean ? quantise8<kFmt, true>(x[it], scale, inv) : quantise8<kFmt, false>(x[it], scale, inv);
+        reinterpret_cast<uint2*>(slab + (size_t)(off + r + it * kRows) * kD)[v] = c;
+        if constexpr (kPool) add_codes8<kFmt>(sum, c);
+      }
+    return scale;
   }
+};
+
+// acc += scale * (sum of the stored codes of a whole page), as the rows above are spread.
+template <int kD, int kFmt>
+__device__ __forceinline__ void add_stored_page(const CacheGeom& g, const uint8_t* slab, float scale, float (&acc)[8]) {
+  constexpr int kVec = kD / 8, kRows = kAppThreads / kVec;
+  float sum[8] = {};
+#pragma unroll 8
+  for (int r = threadIdx.x / kVec; r < g.ps; r += kRows)
+    add_codes8<kFmt>(sum, reinterpret_cast<const uint2*>(slab + (size_t)r * kD)[threadIdx.x % kVec]);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) acc[e] = fmaf(sum[e], scale, acc[e]);
 }
 
-// Mean of block b's stored keys of one head (the whole CTA; every token is in the cache).
-template <int kD, int kFmt>
-__device__ __forceinline__ void pool_cached_block(const CacheGeom& g, const int32_t* __restrict__ table, int b,
-                                                  int head, const uint8_t* Kc, const float* Ks, float* out,
-                                                  float (*red)[kD + 4]) {
-  constexpr int kVec = kD / 16;                      // 16-code vectors of a row
-  constexpr int kGroups = kAppThreads / kVec;        // rows in flight
-  const int v = threadIdx.x % kVec, r0 = threadIdx.x / kVec;
-  float acc[16];
-#pragma unroll
-  for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-#pragma unroll 4
-  for (int t = r0; t < g.bs; t += kGroups) {
-    const int pos = b * g.bs + t;
-    const int32_t page = __ldg(table + pos / g.ps);
-    if (!page_ok(g, page)) {
-      atomicOr(g.err, kErrBadPage);
-      continue;
-    }
-    const float sc = Ks[(size_t)page * g.Hkv + head];
-    const uint4 c = reinterpret_cast<const uint4*>(Kc + slab_offset(g, page, head) + (size_t)(pos % g.ps) * kD)[v];
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 lo = codes2_to_float2<kFmt>(w[e]), hi = codes2_to_float2<kFmt>(w[e] >> 16);
-      acc[4 * e] = fmaf(lo.x, sc, acc[4 * e]);
-      acc[4 * e + 1] = fmaf(lo.y, sc, acc[4 * e + 1]);
-      acc[4 * e + 2] = fmaf(hi.x, sc, acc[4 * e + 2]);
-      acc[4 * e + 3] = fmaf(hi.y, sc, acc[4 * e + 3]);
-    }
-  }
-  // row groups of one warp share a lane pattern: fold them first, then the warps in order
+// The CTA's sums of its columns: part[d] for all d < kD (visible after the caller's next barrier).
+template <int kD>
+__device__ __forceinline__ void fold_columns(float (&acc)[8], AppendSmem<kD>& sm) {
+  constexpr int kVec = kD / 8;
 #pragma unroll
   for (int off = kVec; off < 32; off <<= 1)
 #pragma unroll
-    for (int e = 0; e < 16; ++e) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], off);
-  __syncthreads();
+    for (int e = 0; e < 8; ++e) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], off);
+  __syncthreads();  // an earlier fold is read
   if ((threadIdx.x & 31) < kVec)
 #pragma unroll
-    for (int e = 0; e < 16; ++e) red[threadIdx.x >> 5][v * 16 + e] = acc[e];
+    for (int e = 0; e < 8; ++e) sm.pool[threadIdx.x >> 5][(threadIdx.x & 31) * 8 + e] = acc[e];
   __syncthreads();
   if (threadIdx.x < kD) {
-    float sum = 0.f;
+    float s = 0.f;
 #pragma unroll
-    for (int w = 0; w < kAppThreads / 32; ++w) sum += red[w][threadIdx.x];
-    out[threadIdx.x] = sum / (float)g.bs;
+    for (int w = 0; w < kAppWarps; ++w) s += sm.pool[w][threadIdx.x];
+    sm.part[threadIdx.x] = s;
   }
+}
+
+// One side (K or V) of an append.
+struct AppendSide {
+  const __nv_bfloat16* src;
+  int64_t stride;
+  uint8_t* codes;
+  float* scales;
+};
+
+// Page that a request's token at `pos` (packed row t) goes to, -1 if it is left out.
+__device__ __forceinline__ int32_t page_of_slot(const CacheGeom& g, const int32_t* __restrict__ slots, int32_t t, int off) {
+  const int32_t slot = __ldg(slots + t);
+  if (slot < 0) return -1;
+  if (slot % g.ps == off && page_ok(g, slot / g.ps)) return slot / g.ps;
+  if (threadIdx.x == 0) atomicOr(g.err, kErrBadPage);
+  return -1;
+}
+
+__device__ __forceinline__ int32_t page_of_table(const CacheGeom& g, const int32_t* __restrict__ table, int ordinal) {
+  const int32_t page = __ldg(table + ordinal);
+  if (page_ok(g, page)) return page;
+  if (threadIdx.x == 0) atomicOr(g.err, kErrBadPage);
+  return -1;
 }
 
 template <int kD, int kFmt>
 __global__ void __launch_bounds__(kAppThreads)
-    cache_append_kernel(CacheGeom g, const __nv_bfloat16* __restrict__ K, int64_t k_stride,
-                        const __nv_bfloat16* __restrict__ V, int64_t v_stride, int32_t max_tokens,
+    cache_append_kernel(CacheGeom g, AppendSide sk, AppendSide sv, int32_t max_tokens,
                         const int32_t* __restrict__ cu_new, const int32_t* __restrict__ lens,
-                        const int32_t* __restrict__ slots, const int32_t* __restrict__ tables, uint8_t* Kc,
-                        uint8_t* Vc, float* Ks, float* Vs, float* Kbar) {
-  __shared__ float red[kAppThreads / 32];
-  __shared__ float pool_red[kAppThreads / 32][kD + 4];
+                        const int32_t* __restrict__ slots, const int32_t* __restrict__ tables, float* Kbar) {
+  __shared__ AppendSmem<kD> sm;
   const int head = blockIdx.x, s = blockIdx.y;
   const bool is_v = blockIdx.z != 0;
+  const AppendSide a = is_v ? sv : sk;
   const int32_t t0 = max(__ldg(cu_new + s), 0), t1 = min(__ldg(cu_new + s + 1), max_tokens);
   const int32_t len = cached_len(g, lens, s), n = t1 - t0, start = len - n;
   if (n <= 0 || start < 0) return;
-  const __nv_bfloat16* src = (is_v ? V : K) + (size_t)head * kD;
-  const int64_t stride = is_v ? v_stride : k_stride;
+  int turn = 0;
   for (int32_t pos = start; pos < len;) {
     const int off = pos % g.ps, nr = min(g.ps - off, len - pos);
-    const int32_t t = t0 + (pos - start), slot = __ldg(slots + t);
-    const int32_t page = slot / g.ps;
-    if (slot >= 0 && slot % g.ps == off && page_ok(g, page)) {
-      const size_t at = (size_t)page * g.Hkv + head;
-      quantise_rows<kD, kFmt>(src + (int64_t)t * stride, stride, nr, off, (is_v ? Vc : Kc) + slab_offset(g, page, head),
-                              (is_v ? Vs : Ks) + at, red);
-    } else if (slot >= 0 && threadIdx.x == 0) {
-      atomicOr(g.err, kErrBadPage);
+    const int32_t t = t0 + (pos - start), page = page_of_slot(g, slots, t, off);
+    if (page >= 0) {
+      PageRows<kD, kFmt, 128 * kD / 8 / kAppThreads> rows;  // any page size
+      float unused[8];
+      rows.load(a.src + (size_t)head * kD + (int64_t)t * a.stride, a.stride, nr);
+      rows.template store<false>(nr, off, a.codes + slab_offset(g, page, head), a.scales + (size_t)page * g.Hkv + head,
+                                 sm.red, turn, unused);
     }
     pos += nr;
   }
   if (is_v) return;
-  __syncthreads();  // the codes are visible to the whole CTA
-  for (int b = start / g.bs; b < len / g.bs; ++b)
-    pool_cached_block<kD, kFmt>(g, tables + (size_t)s * g.MP, b, head, Kc, Ks,
-                                Kbar + (((size_t)s * g.MB + b) * g.Hkv + head) * kD, pool_red);
+  __syncthreads();  // the codes and scales are visible to the whole CTA
+  for (int b = start / g.bs; b < len / g.bs; ++b) {
+    float acc[8] = {};
+    for (int pi = b * g.bs / g.ps; pi < (b + 1) * g.bs / g.ps; ++pi) {
+      const int32_t page = page_of_table(g, tables + (size_t)s * g.MP, pi);
+      if (page >= 0)
+        add_stored_page<kD, kFmt>(g, a.codes + slab_offset(g, page, head), a.scales[(size_t)page * g.Hkv + head], acc);
+    }
+    fold_columns<kD>(acc, sm);
+    if (threadIdx.x < kD)
+      Kbar[(((size_t)s * g.MB + b) * g.Hkv + head) * kD + threadIdx.x] = sm.part[threadIdx.x] / (float)g.bs;
+  }
+}
+
+// Work items are numbered so that request s has floor(n / bs) + 2 of them (as many MoBA blocks as n
+// tokens can touch), from floor(cu_new[s] / bs) + 2 s on.
+__device__ __forceinline__ int first_item(int32_t cu, int s, int bs) { return cu / bs + 2 * s; }
+
+// kIt: vectors of a page that a thread holds; the next page is loaded while this one is written.
+template <int kD, int kFmt, int kIt>
+__global__ void __launch_bounds__(kAppThreads)
+    cache_prompt_kernel(CacheGeom g, AppendSide sk, AppendSide sv, int32_t max_tokens, int ranks,
+                        const int32_t* __restrict__ cu_new, const int32_t* __restrict__ lens,
+                        const int32_t* __restrict__ slots, const int32_t* __restrict__ tables, float* Kbar) {
+  __shared__ AppendSmem<kD> sm;
+  const int item = blockIdx.x / ranks, rank = blockIdx.x % ranks, head = blockIdx.y;
+  const bool is_v = blockIdx.z != 0;
+  const AppendSide a = is_v ? sv : sk;
+  int s = 0;  // the last request whose items start at or before this one
+  for (int hi = g.B - 1; s < hi;) {
+    const int mid = (s + hi + 1) >> 1;
+    if (first_item(max(__ldg(cu_new + mid), 0), mid, g.bs) <= item) s = mid; else hi = mid - 1;
+  }
+  const int32_t t0 = max(__ldg(cu_new + s), 0), t1 = min(__ldg(cu_new + s + 1), max_tokens);
+  const int32_t len = cached_len(g, lens, s), n = t1 - t0, start = len - n;
+  const int b = start / g.bs + (item - first_item(t0, s, g.bs));
+  if (n <= 0 || start < 0 || b < 0 || (int64_t)b * g.bs >= len) return;  // the same for the whole cluster
+  const bool pool = !is_v && (int64_t)(b + 1) * g.bs <= len;
+  const int R = g.bs / g.ps, per = (R + ranks - 1) / ranks;
+  const int p0 = b * R + rank * per, p1 = b * R + min(R, (rank + 1) * per);
+  // new rows of page ordinal p: packed row of the first, how many, and the older rows before them
+  auto rows_of = [&](int p, int32_t& t, int& nr, int& off) {
+    const int32_t lo = max(start, p * g.ps), hi = min(len, (p + 1) * g.ps);
+    t = t0 + (lo - start);
+    off = lo - p * g.ps;
+    nr = max(hi - lo, 0);
+  };
+  PageRows<kD, kFmt, kIt> cur, nxt;
+  int32_t t, page = -1;
+  int nr = 0, off = 0, turn = 0;
+  float acc[8] = {};
+  auto fetch = [&](int p, PageRows<kD, kFmt, kIt>& rows, int32_t& pg, int& n_, int& o_) {
+    n_ = 0;
+    pg = -1;
+    if (p >= p1) return;
+    rows_of(p, t, n_, o_);
+    if (n_ == 0) return;
+    rows.load(a.src + (size_t)head * kD + (int64_t)t * a.stride, a.stride, n_);
+    pg = page_of_slot(g, slots, t, o_);
+  };
+  fetch(p0, cur, page, nr, off);
+  for (int p = p0; p < p1; ++p) {
+    int32_t page_n;
+    int nr_n, off_n = 0;
+    fetch(p + 1, nxt, page_n, nr_n, off_n);
+    float* sp = a.scales + (size_t)max(page, 0) * g.Hkv + head;
+    uint8_t* slab = a.codes + slab_offset(g, max(page, 0), head);
+    // the pooled key is that of the pages that the block table names
+    const int32_t listed = pool ? page_of_table(g, tables + (size_t)s * g.MP, p) : -1;
+    if (pool && page >= 0 && page == listed && off == 0) {
+      float sum[8] = {};
+      const float scale = cur.template store<true>(nr, off, slab, sp, sm.red, turn, sum);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = fmaf(sum[e], scale, acc[e]);
+    } else {
+      float unused[8];
+      if (page >= 0) cur.template store<false>(nr, off, slab, sp, sm.red, turn, unused);
+      if (pool) {  // older rows are in the page: read all of it back
+        __syncthreads();
+        if (listed >= 0)
+          add_stored_page<kD, kFmt>(g, a.codes + slab_offset(g, listed, head), a.scales[(size_t)listed * g.Hkv + head],
+                                    acc);
+      }
+    }
+    cur = nxt;
+    page = page_n;
+    nr = nr_n;
+    off = off_n;
+  }
+  if (!pool) return;  // the same for the whole cluster
+  fold_columns<kD>(acc, sm);
+  cluster_barrier();
+  if (rank == 0 && threadIdx.x < kD) {
+    float total = sm.part[threadIdx.x];
+    for (int r = 1; r < ranks; ++r) total += ld_cluster_f32(&sm.part[threadIdx.x], r);
+    Kbar[(((size_t)s * g.MB + b) * g.Hkv + head) * kD + threadIdx.x] = total / (float)g.bs;
+  }
+  cluster_barrier();  // no CTA leaves while its share is read
+}
+
+template <int kD, int kFmt, int kIt>
+cudaError_t launch_prompt(const CacheGeom& g, const AppendSide& sk, const AppendSide& sv, int32_t max_tokens,
+                          const int32_t* cu_new, const int32_t* lens, const int32_t* slots, const int32_t* tables,
+                          float* Kbar, cudaStream_t st) {
+  const int rows = g.ps > 128 ? g.ps : 128;  // of a CTA, at the least
+  int ranks = 1;
+  while (ranks < 8 && 2 * ranks * rows <= g.bs) ranks *= 2;
+  const int64_t items = max_tokens / g.bs + 2 * (int64_t)g.B;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(items * ranks), (unsigned)g.Hkv, 2);
+  cfg.blockDim = dim3(kAppThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)ranks;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_prompt_kernel<kD, kFmt, kIt>, g, sk, sv, max_tokens, ranks, cu_new, lens, slots,
+                            tables, Kbar);
+}
+
+template <int kD, int kFmt>
+cudaError_t launch_append_t(const CacheGeom& g, const AppendSide& sk, const AppendSide& sv, int32_t max_tokens,
+                            const int32_t* cu_new, const int32_t* lens, const int32_t* slots, const int32_t* tables,
+                            float* Kbar, cudaStream_t st) {
+  // A few tokens for each slot (decode steps, drafts): one CTA a request, no empty clusters to start.
+  if (max_tokens <= 4 * (int64_t)g.B) {
+    cache_append_kernel<kD, kFmt><<<dim3((unsigned)g.Hkv, (unsigned)g.B, 2), kAppThreads, 0, st>>>(
+        g, sk, sv, max_tokens, cu_new, lens, slots, tables, Kbar);
+    return cudaGetLastError();
+  }
+  auto go = [&](auto fn) { return fn(g, sk, sv, max_tokens, cu_new, lens, slots, tables, Kbar, st); };
+  const int each = g.ps * (kD / 8) / kAppThreads;  // vectors of a page for each thread
+  if constexpr (kD == 128)
+    if (each == 8) return go(launch_prompt<kD, kFmt, 8>);
+  switch (each) {
+    case 4: return go(launch_prompt<kD, kFmt, 4>);
+    case 2: return go(launch_prompt<kD, kFmt, 2>);
+    default: return go(launch_prompt<kD, kFmt, 1>);
+  }
 }
 
 }  // namespace
@@ -202,15 +423,11 @@ cudaError_t launch_cache_append(const CacheGeom& g, const __nv_bfloat16* K, int6
                                 int64_t v_stride, int32_t max_tokens, const int32_t* cu_new, const int32_t* lens,
                                 const int32_t* slots, const int32_t* tables, uint8_t* Kc, uint8_t* Vc, float* Ks,
                                 float* Vs, float* Kbar, cudaStream_t st) {
-  const dim3 grid((unsigned)g.Hkv, (unsigned)g.B, 2);
-  auto go = [&](auto kernel) {
-    kernel<<<grid, kAppThreads, 0, st>>>(g, K, k_stride, V, v_stride, max_tokens, cu_new, lens, slots, tables, Kc, Vc,
-                                         Ks, Vs, Kbar);
-    return cudaGetLastError();
-  };
+  const AppendSide sk{K, k_stride, Kc, Ks}, sv{V, v_stride, Vc, Vs};
+  auto go = [&](auto fn) { return fn(g, sk, sv, max_tokens, cu_new, lens, slots, tables, Kbar, st); };
   if (g.D == 64)
-    return g.fmt == MOBA_CACHE_E4M3 ? go(cache_append_kernel<64, MOBA_CACHE_E4M3>) : go(cache_append_kernel<64, MOBA_CACHE_INT8>);
-  return g.fmt == MOBA_CACHE_E4M3 ? go(cache_append_kernel<128, MOBA_CACHE_E4M3>) : go(cache_append_kernel<128, MOBA_CACHE_INT8>);
+    return g.fmt == MOBA_CACHE_E4M3 ? go(launch_append_t<64, MOBA_CACHE_E4M3>) : go(launch_append_t<64, MOBA_CACHE_INT8>);
+  return g.fmt == MOBA_CACHE_E4M3 ? go(launch_append_t<128, MOBA_CACHE_E4M3>) : go(launch_append_t<128, MOBA_CACHE_INT8>);
 }
 
 }  // namespace moba

@@ -33,10 +33,6 @@ __device__ __forceinline__ bool ranks_before(double sa, int32_t ba, double sb, i
   return sa > sb || (sa == sb && ba < bb);
 }
 
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // Sum of v[x] over the warp's lanes, for all 32 x at once: lane x returns the sum of v[x].  Each
 // step halves the values a lane still carries: 31 exchanges instead of 5 for every value.
 __device__ __forceinline__ double warp_sums(double (&v)[32]) {
