@@ -119,6 +119,23 @@ struct PageRows {
   static constexpr int kVec = kD / 8, kRows = kAppThreads / kVec;
   uint4 x[kIt];
 
+  // Asynchronously into a stage of the thread's own in shared memory (rows behind nr as zeros), and
+  // from there: no thread reads what another one copied, so no barrier is needed.
+  static __device__ __forceinline__ void prefetch(uint32_t stage, const __nv_bfloat16* __restrict__ src, int64_t stride,
+                                                  int nr) {
+    const int v = threadIdx.x % kVec, r = threadIdx.x / kVec;
+#pragma unroll
+    for (int it = 0; it < kIt; ++it) {
+      const bool live = r + it * kRows < nr;
+      cp_async_16(stage + (it * kAppThreads + threadIdx.x) * 16,
+                  src + (live ? (int64_t)(r + it * kRows) * stride + v * 8 : 0), live ? 16 : 0);
+    }
+  }
+  __device__ __forceinline__ void take(uint32_t stage) {
+#pragma unroll
+    for (int it = 0; it < kIt; ++it) x[it] = ld_shared_16(stage + (it * kAppThreads + threadIdx.x) * 16);
+  }
+
   __device__ __forceinline__ void load(const __nv_bfloat16* __restrict__ src, int64_t stride, int nr) {
     const int v = threadIdx.x % kVec, r = threadIdx.x / kVec;
 #pragma unroll
@@ -292,21 +309,34 @@ __global__ void __launch_bounds__(kAppThreads)
 // tokens can touch), from floor(cu_new[s] / bs) + 2 s on.
 __device__ __forceinline__ int first_item(int32_t cu, int s, int bs) { return cu / bs + 2 * s; }
 
-// kIt: vectors of a page that a thread holds; the next page is loaded while this one is written.
-template <int kD, int kFmt, int kIt>
-__global__ void __launch_bounds__(kAppThreads)
+// Last request whose items start at or before `item` (a warp narrows the range to 1 / 32 a step).
+__device__ __forceinline__ int request_of_item(const CacheGeom& g, const int32_t* __restrict__ cu_new, int item) {
+  int lo = 0, n = g.B;
+  while (n > 1) {
+    const int step = (n + 31) / 32, x = lo + (int)(threadIdx.x & 31) * step;
+    const bool at = x < lo + n && first_item(max(__ldg(cu_new + min(x, g.B - 1)), 0), x, g.bs) <= item;
+    const int below = __popc(__ballot_sync(0xffffffffu, at));
+    const int next = lo + max(below - 1, 0) * step;
+    n = min(step, lo + n - next);
+    lo = next;
+  }
+  return lo;
+}
+
+// kIt: vectors of a page that a thread holds; kAhead: pages on their way while one is written.
+template <int kD, int kFmt, int kIt, int kAhead>
+__global__ void __launch_bounds__(kAppThreads, 3)
     cache_prompt_kernel(CacheGeom g, AppendSide sk, AppendSide sv, int32_t max_tokens, int ranks,
                         const int32_t* __restrict__ cu_new, const int32_t* __restrict__ lens,
                         const int32_t* __restrict__ slots, const int32_t* __restrict__ tables, float* Kbar) {
+  using Rows = PageRows<kD, kFmt, kIt>;
+  constexpr uint32_t kStageBytes = kIt * kAppThreads * 16;
   __shared__ AppendSmem<kD> sm;
+  extern __shared__ __align__(16) uint8_t stages[];
   const int item = blockIdx.x / ranks, rank = blockIdx.x % ranks, head = blockIdx.y;
   const bool is_v = blockIdx.z != 0;
   const AppendSide a = is_v ? sv : sk;
-  int s = 0;  // the last request whose items start at or before this one
-  for (int hi = g.B - 1; s < hi;) {
-    const int mid = (s + hi + 1) >> 1;
-    if (first_item(max(__ldg(cu_new + mid), 0), mid, g.bs) <= item) s = mid; else hi = mid - 1;
-  }
+  const int s = request_of_item(g, cu_new, item);
   const int32_t t0 = max(__ldg(cu_new + s), 0), t1 = min(__ldg(cu_new + s + 1), max_tokens);
   const int32_t len = cached_len(g, lens, s), n = t1 - t0, start = len - n;
   const int b = start / g.bs + (item - first_item(t0, s, g.bs));
@@ -314,43 +344,54 @@ __global__ void __launch_bounds__(kAppThreads)
   const bool pool = !is_v && (int64_t)(b + 1) * g.bs <= len;
   const int R = g.bs / g.ps, per = (R + ranks - 1) / ranks;
   const int p0 = b * R + rank * per, p1 = b * R + min(R, (rank + 1) * per);
+  const __nv_bfloat16* src = a.src + (size_t)head * kD;
   // new rows of page ordinal p: packed row of the first, how many, and the older rows before them
   auto rows_of = [&](int p, int32_t& t, int& nr, int& off) {
     const int32_t lo = max(start, p * g.ps), hi = min(len, (p + 1) * g.ps);
     t = t0 + (lo - start);
     off = lo - p * g.ps;
-    nr = max(hi - lo, 0);
+    nr = p < p1 ? max(hi - lo, 0) : 0;
   };
-  PageRows<kD, kFmt, kIt> cur, nxt;
-  int32_t t, page = -1;
-  int nr = 0, off = 0, turn = 0;
+  const uint32_t ring = smem_u32(stages);
+  auto prefetch = [&](int p, int stage) {
+    int32_t t;
+    int nr, off;
+    rows_of(p, t, nr, off);
+    if (nr > 0) Rows::prefetch(ring + stage * kStageBytes, src + (int64_t)t * a.stride, a.stride, nr);
+    cp_async_commit();
+  };
+  auto slot_page = [&](int p) {
+    int32_t t;
+    int nr, off;
+    rows_of(p, t, nr, off);
+    return nr > 0 ? page_of_slot(g, slots, t, off) : -1;
+  };
+#pragma unroll
+  for (int q = 0; q < kAhead; ++q) prefetch(p0 + q, q);
+  int turn = 0, stage = 0;
+  int32_t page = slot_page(p0);
   float acc[8] = {};
-  auto fetch = [&](int p, PageRows<kD, kFmt, kIt>& rows, int32_t& pg, int& n_, int& o_) {
-    n_ = 0;
-    pg = -1;
-    if (p >= p1) return;
-    rows_of(p, t, n_, o_);
-    if (n_ == 0) return;
-    rows.load(a.src + (size_t)head * kD + (int64_t)t * a.stride, a.stride, n_);
-    pg = page_of_slot(g, slots, t, o_);
-  };
-  fetch(p0, cur, page, nr, off);
   for (int p = p0; p < p1; ++p) {
-    int32_t page_n;
-    int nr_n, off_n = 0;
-    fetch(p + 1, nxt, page_n, nr_n, off_n);
-    float* sp = a.scales + (size_t)max(page, 0) * g.Hkv + head;
-    uint8_t* slab = a.codes + slab_offset(g, max(page, 0), head);
+    prefetch(p + kAhead, stage == 0 ? kAhead : stage - 1);  // the stage that the last page left
+    const int32_t page_n = slot_page(p + 1);
     // the pooled key is that of the pages that the block table names
     const int32_t listed = pool ? page_of_table(g, tables + (size_t)s * g.MP, p) : -1;
+    int32_t t;
+    int nr, off;
+    rows_of(p, t, nr, off);
+    cp_async_wait<kAhead>();
+    Rows rows;
+    if (page >= 0) rows.take(ring + stage * kStageBytes);
+    float* sp = a.scales + (size_t)max(page, 0) * g.Hkv + head;
+    uint8_t* slab = a.codes + slab_offset(g, max(page, 0), head);
     if (pool && page >= 0 && page == listed && off == 0) {
       float sum[8] = {};
-      const float scale = cur.template store<true>(nr, off, slab, sp, sm.red, turn, sum);
+      const float scale = rows.template store<true>(nr, off, slab, sp, sm.red, turn, sum);
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc[e] = fmaf(sum[e], scale, acc[e]);
     } else {
       float unused[8];
-      if (page >= 0) cur.template store<false>(nr, off, slab, sp, sm.red, turn, unused);
+      if (page >= 0) rows.template store<false>(nr, off, slab, sp, sm.red, turn, unused);
       if (pool) {  // older rows are in the page: read all of it back
         __syncthreads();
         if (listed >= 0)
@@ -358,10 +399,8 @@ __global__ void __launch_bounds__(kAppThreads)
                                     acc);
       }
     }
-    cur = nxt;
     page = page_n;
-    nr = nr_n;
-    off = off_n;
+    stage = stage == kAhead ? 0 : stage + 1;
   }
   if (!pool) return;  // the same for the whole cluster
   fold_columns<kD>(acc, sm);
@@ -374,7 +413,7 @@ __global__ void __launch_bounds__(kAppThreads)
   cluster_barrier();  // no CTA leaves while its share is read
 }
 
-template <int kD, int kFmt, int kIt>
+template <int kD, int kFmt, int kIt, int kAhead>
 cudaError_t launch_prompt(const CacheGeom& g, const AppendSide& sk, const AppendSide& sv, int32_t max_tokens,
                           const int32_t* cu_new, const int32_t* lens, const int32_t* slots, const int32_t* tables,
                           float* Kbar, cudaStream_t st) {
@@ -385,14 +424,18 @@ cudaError_t launch_prompt(const CacheGeom& g, const AppendSide& sk, const Append
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(items * ranks), (unsigned)g.Hkv, 2);
   cfg.blockDim = dim3(kAppThreads);
+  cfg.dynamicSmemBytes = (kAhead + 1) * kIt * kAppThreads * 16;
   cfg.stream = st;
+  auto kernel = cache_prompt_kernel<kD, kFmt, kIt, kAhead>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+  if (e != cudaSuccess) return e;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = (unsigned)ranks;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_prompt_kernel<kD, kFmt, kIt>, g, sk, sv, max_tokens, ranks, cu_new, lens, slots,
+  return cudaLaunchKernelEx(&cfg, kernel, g, sk, sv, max_tokens, ranks, cu_new, lens, slots,
                             tables, Kbar);
 }
 
@@ -409,11 +452,11 @@ cudaError_t launch_append_t(const CacheGeom& g, const AppendSide& sk, const Appe
   auto go = [&](auto fn) { return fn(g, sk, sv, max_tokens, cu_new, lens, slots, tables, Kbar, st); };
   const int each = g.ps * (kD / 8) / kAppThreads;  // vectors of a page for each thread
   if constexpr (kD == 128)
-    if (each == 8) return go(launch_prompt<kD, kFmt, 8>);
+    if (each == 8) return go(launch_prompt<kD, kFmt, 8, 1>);
   switch (each) {
-    case 4: return go(launch_prompt<kD, kFmt, 4>);
-    case 2: return go(launch_prompt<kD, kFmt, 2>);
-    default: return go(launch_prompt<kD, kFmt, 1>);
+    case 4: return go(launch_prompt<kD, kFmt, 4, 2>);
+    case 2: return go(launch_prompt<kD, kFmt, 2, 3>);
+    default: return go(launch_prompt<kD, kFmt, 1, 5>);
   }
 }
 
