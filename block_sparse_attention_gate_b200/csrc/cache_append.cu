@@ -25,7 +25,8 @@
 namespace moba {
 namespace {
 
-constexpr int kAppThreads = 256, kAppWarps = kAppThreads / 32;
+constexpr int kStepThreads = 256, kPromptThreads = 128;  // of the two kernels
+constexpr int kMaxWarps = kStepThreads / 32;
 constexpr float kTiny = 0x1p-96f;  // keeps scales and quotients far from the subnormal range
 constexpr uint32_t kInfBits = 0x7f80;  // magnitude bits of a bf16 infinity; NaN lies above
 
@@ -95,28 +96,29 @@ __device__ __forceinline__ void add_codes8(float (&sum)[8], const uint2& c) {
 
 // Largest magnitude (bf16 bits) over the block; red holds one value a warp and is used by one call
 // out of two, so that one barrier a call is enough.
+template <int kThreads>
 __device__ __forceinline__ uint32_t block_max(uint32_t x, uint32_t* red) {
   x = __reduce_max_sync(0xffffffffu, x);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
   __syncthreads();
   x = red[0];
 #pragma unroll
-  for (int w = 1; w < kAppWarps; ++w) x = max(x, red[w]);
+  for (int w = 1; w < kThreads / 32; ++w) x = max(x, red[w]);
   return x;
 }
 
 // Shared memory of a CTA.
 template <int kD>
 struct AppendSmem {
-  uint32_t red[2][kAppWarps];
-  float pool[kAppWarps][kD];
+  uint32_t red[2][kMaxWarps];
+  float pool[kMaxWarps][kD];
   float part[kD];  // this CTA's share of a pooled key
 };
 
 // The rows of one (page, KV head): thread holds vector v (8 columns) of rows r + it * kRows.
-template <int kD, int kFmt, int kIt>
+template <int kD, int kFmt, int kIt, int kThreads>
 struct PageRows {
-  static constexpr int kVec = kD / 8, kRows = kAppThreads / kVec;
+  static constexpr int kVec = kD / 8, kRows = kThreads / kVec;
   uint4 x[kIt];
 
   // Asynchronously into a stage of the thread's own in shared memory (rows behind nr as zeros), and
@@ -127,13 +129,13 @@ struct PageRows {
 #pragma unroll
     for (int it = 0; it < kIt; ++it) {
       const bool live = r + it * kRows < nr;
-      cp_async_16(stage + (it * kAppThreads + threadIdx.x) * 16,
+      cp_async_16(stage + (it * kThreads + threadIdx.x) * 16,
                   src + (live ? (int64_t)(r + it * kRows) * stride + v * 8 : 0), live ? 16 : 0);
     }
   }
   __device__ __forceinline__ void take(uint32_t stage) {
 #pragma unroll
-    for (int it = 0; it < kIt; ++it) x[it] = ld_shared_16(stage + (it * kAppThreads + threadIdx.x) * 16);
+    for (int it = 0; it < kIt; ++it) x[it] = ld_shared_16(stage + (it * kThreads + threadIdx.x) * 16);
   }
 
   __device__ __forceinline__ void load(const __nv_bfloat16* __restrict__ src, int64_t stride, int nr) {
@@ -148,7 +150,7 @@ struct PageRows {
 
   // Into rows [off, off + nr) of the slab.  kPool: sum += codes of the new rows.  Returns the scale.
   template <bool kPool>
-  __device__ __forceinline__ float store(int nr, int off, uint8_t* slab, float* scale_ptr, uint32_t (*red)[kAppWarps],
+  __device__ __forceinline__ float store(int nr, int off, uint8_t* slab, float* scale_ptr, uint32_t (*red)[kMaxWarps],
                                          int& turn, float (&sum)[8]) {
     const int v = threadIdx.x % kVec, r = threadIdx.x / kVec;
     uint32_t big2 = 0;  // two magnitudes side by side
@@ -158,7 +160,7 @@ struct PageRows {
       const uint32_t b = __vmaxu2(x[it].z & 0x7fff7fffu, x[it].w & 0x7fff7fffu);
       big2 = __vmaxu2(big2, __vmaxu2(a, b));
     }
-    uint32_t big = block_max(max(big2 & 0xffffu, big2 >> 16), red[turn ^= 1]);
+    uint32_t big = block_max<kThreads>(max(big2 & 0xffffu, big2 >> 16), red[turn ^= 1]);
     const bool clean = big < kInfBits;
     if (!clean) {  // the scale is that of the finite values
       big = 0;
@@ -171,7 +173,7 @@ struct PageRows {
           big = max(big, max(lo < kInfBits ? lo : 0u, hi < kInfBits ? hi : 0u));
         }
       }
-      big = block_max(big, red[turn ^= 1]);
+      big = block_max<kThreads>(big, red[turn ^= 1]);
     }
     float scale = scale_for<kFmt>(__uint_as_float(big << 16));
     if (off > 0) {
@@ -180,7 +182,7 @@ struct PageRows {
       __syncthreads();  // every thread has read the old scale
       if (old < scale) {
         uint2* rows = reinterpret_cast<uint2*>(slab);
-        for (int i = threadIdx.x; i < off * kVec; i += kAppThreads) {
+        for (int i = threadIdx.x; i < off * kVec; i += kThreads) {
           const uint2 c = rows[i];
           const uint32_t in[2] = {c.x, c.y};
           uint32_t out[2];
@@ -209,9 +211,9 @@ struct PageRows {
 };
 
 // acc += scale * (sum of the stored codes of a whole page), as the rows above are spread.
-template <int kD, int kFmt>
+template <int kD, int kFmt, int kThreads>
 __device__ __forceinline__ void add_stored_page(const CacheGeom& g, const uint8_t* slab, float scale, float (&acc)[8]) {
-  constexpr int kVec = kD / 8, kRows = kAppThreads / kVec;
+  constexpr int kVec = kD / 8, kRows = kThreads / kVec;
   float sum[8] = {};
 #pragma unroll 8
   for (int r = threadIdx.x / kVec; r < g.ps; r += kRows)
@@ -220,23 +222,24 @@ __device__ __forceinline__ void add_stored_page(const CacheGeom& g, const uint8_
   for (int e = 0; e < 8; ++e) acc[e] = fmaf(sum[e], scale, acc[e]);
 }
 
-// The CTA's sums of its columns: part[d] for all d < kD (visible after the caller's next barrier).
-template <int kD>
-__device__ __forceinline__ void fold_columns(float (&acc)[8], AppendSmem<kD>& sm) {
-  constexpr int kVec = kD / 8;
+// The CTA's sums of its columns (kN of them in each lane): part[d] for all d < kD, visible after the
+// caller's next barrier.
+template <int kD, int kN, int kThreads>
+__device__ __forceinline__ void fold_columns(float (&acc)[kN], AppendSmem<kD>& sm) {
+  constexpr int kVec = kD / kN;
 #pragma unroll
   for (int off = kVec; off < 32; off <<= 1)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], off);
+    for (int e = 0; e < kN; ++e) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], off);
   __syncthreads();  // an earlier fold is read
   if ((threadIdx.x & 31) < kVec)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sm.pool[threadIdx.x >> 5][(threadIdx.x & 31) * 8 + e] = acc[e];
+    for (int e = 0; e < kN; ++e) sm.pool[threadIdx.x >> 5][(threadIdx.x & 31) * kN + e] = acc[e];
   __syncthreads();
   if (threadIdx.x < kD) {
     float s = 0.f;
 #pragma unroll
-    for (int w = 0; w < kAppWarps; ++w) s += sm.pool[w][threadIdx.x];
+    for (int w = 0; w < kThreads / 32; ++w) s += sm.pool[w][threadIdx.x];
     sm.part[threadIdx.x] = s;
   }
 }
@@ -266,7 +269,7 @@ __device__ __forceinline__ int32_t page_of_table(const CacheGeom& g, const int32
 }
 
 template <int kD, int kFmt>
-__global__ void __launch_bounds__(kAppThreads)
+__global__ void __launch_bounds__(kStepThreads)
     cache_append_kernel(CacheGeom g, AppendSide sk, AppendSide sv, int32_t max_tokens,
                         const int32_t* __restrict__ cu_new, const int32_t* __restrict__ lens,
                         const int32_t* __restrict__ slots, const int32_t* __restrict__ tables, float* Kbar) {
@@ -282,7 +285,7 @@ __global__ void __launch_bounds__(kAppThreads)
     const int off = pos % g.ps, nr = min(g.ps - off, len - pos);
     const int32_t t = t0 + (pos - start), page = page_of_slot(g, slots, t, off);
     if (page >= 0) {
-      PageRows<kD, kFmt, 128 * kD / 8 / kAppThreads> rows;  // any page size
+      PageRows<kD, kFmt, 128 * kD / 8 / kStepThreads, kStepThreads> rows;  // any page size
       float unused[8];
       rows.load(a.src + (size_t)head * kD + (int64_t)t * a.stride, a.stride, nr);
       rows.template store<false>(nr, off, a.codes + slab_offset(g, page, head), a.scales + (size_t)page * g.Hkv + head,
@@ -292,14 +295,30 @@ __global__ void __launch_bounds__(kAppThreads)
   }
   if (is_v) return;
   __syncthreads();  // the codes and scales are visible to the whole CTA
+  // a warp takes every eighth page of a completed block, 32 rows of it at a time
+  constexpr int kVec = kD / 16, kRows = 32 / kVec;
+  const int warp = threadIdx.x >> 5, v = (threadIdx.x & 31) % kVec, r0 = (threadIdx.x & 31) / kVec;
   for (int b = start / g.bs; b < len / g.bs; ++b) {
-    float acc[8] = {};
-    for (int pi = b * g.bs / g.ps; pi < (b + 1) * g.bs / g.ps; ++pi) {
-      const int32_t page = page_of_table(g, tables + (size_t)s * g.MP, pi);
-      if (page >= 0)
-        add_stored_page<kD, kFmt>(g, a.codes + slab_offset(g, page, head), a.scales[(size_t)page * g.Hkv + head], acc);
+    float acc[16] = {};
+    for (int pi = b * (g.bs / g.ps) + warp; pi < (b + 1) * (g.bs / g.ps); pi += kStepThreads / 32) {
+      const int32_t page = __ldg(tables + (size_t)s * g.MP + pi);
+      if (!page_ok(g, page)) {
+        if ((threadIdx.x & 31) == 0) atomicOr(g.err, kErrBadPage);
+        continue;
+      }
+      const float scale = a.scales[(size_t)page * g.Hkv + head];
+      const uint4* src = reinterpret_cast<const uint4*>(a.codes + slab_offset(g, page, head)) + v;
+      float sum[2][8] = {};
+#pragma unroll 8
+      for (int r = r0; r < g.ps; r += kRows) {
+        const uint4 c = src[r * kVec];
+        add_codes8<kFmt>(sum[0], make_uint2(c.x, c.y));
+        add_codes8<kFmt>(sum[1], make_uint2(c.z, c.w));
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[e] = fmaf(sum[e >> 3][e & 7], scale, acc[e]);
     }
-    fold_columns<kD>(acc, sm);
+    fold_columns<kD, 16, kStepThreads>(acc, sm);
     if (threadIdx.x < kD)
       Kbar[(((size_t)s * g.MB + b) * g.Hkv + head) * kD + threadIdx.x] = sm.part[threadIdx.x] / (float)g.bs;
   }
@@ -323,14 +342,16 @@ __device__ __forceinline__ int request_of_item(const CacheGeom& g, const int32_t
   return lo;
 }
 
-// kIt: vectors of a page that a thread holds; kAhead: pages on their way while one is written.
-template <int kD, int kFmt, int kIt, int kAhead>
-__global__ void __launch_bounds__(kAppThreads, 3)
+// kPS: tokens of a page; kAhead: pages on their way while one is written.
+template <int kD, int kFmt, int kPS, int kAhead>
+__global__ void __launch_bounds__(kPromptThreads, kPS == 128 ? 3 : 4)
     cache_prompt_kernel(CacheGeom g, AppendSide sk, AppendSide sv, int32_t max_tokens, int ranks,
                         const int32_t* __restrict__ cu_new, const int32_t* __restrict__ lens,
                         const int32_t* __restrict__ slots, const int32_t* __restrict__ tables, float* Kbar) {
-  using Rows = PageRows<kD, kFmt, kIt>;
-  constexpr uint32_t kStageBytes = kIt * kAppThreads * 16;
+  constexpr int kIt = kPS * (kD / 8) / kPromptThreads;
+  using Rows = PageRows<kD, kFmt, kIt, kPromptThreads>;
+  constexpr uint32_t kStageBytes = kIt * kPromptThreads * 16;
+  g.ps = kPS;
   __shared__ AppendSmem<kD> sm;
   extern __shared__ __align__(16) uint8_t stages[];
   const int item = blockIdx.x / ranks, rank = blockIdx.x % ranks, head = blockIdx.y;
@@ -395,15 +416,15 @@ __global__ void __launch_bounds__(kAppThreads, 3)
       if (pool) {  // older rows are in the page: read all of it back
         __syncthreads();
         if (listed >= 0)
-          add_stored_page<kD, kFmt>(g, a.codes + slab_offset(g, listed, head), a.scales[(size_t)listed * g.Hkv + head],
-                                    acc);
+          add_stored_page<kD, kFmt, kPromptThreads>(g, a.codes + slab_offset(g, listed, head),
+                                                    a.scales[(size_t)listed * g.Hkv + head], acc);
       }
     }
     page = page_n;
     stage = stage == kAhead ? 0 : stage + 1;
   }
   if (!pool) return;  // the same for the whole cluster
-  fold_columns<kD>(acc, sm);
+  fold_columns<kD, 8, kPromptThreads>(acc, sm);
   cluster_barrier();
   if (rank == 0 && threadIdx.x < kD) {
     float total = sm.part[threadIdx.x];
@@ -413,20 +434,20 @@ __global__ void __launch_bounds__(kAppThreads, 3)
   cluster_barrier();  // no CTA leaves while its share is read
 }
 
-template <int kD, int kFmt, int kIt, int kAhead>
+template <int kD, int kFmt, int kPS, int kAhead>
 cudaError_t launch_prompt(const CacheGeom& g, const AppendSide& sk, const AppendSide& sv, int32_t max_tokens,
                           const int32_t* cu_new, const int32_t* lens, const int32_t* slots, const int32_t* tables,
                           float* Kbar, cudaStream_t st) {
-  const int rows = g.ps > 128 ? g.ps : 128;  // of a CTA, at the least
+  const int rows = 128;  // of a CTA, at the least
   int ranks = 1;
   while (ranks < 8 && 2 * ranks * rows <= g.bs) ranks *= 2;
   const int64_t items = max_tokens / g.bs + 2 * (int64_t)g.B;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(items * ranks), (unsigned)g.Hkv, 2);
-  cfg.blockDim = dim3(kAppThreads);
-  cfg.dynamicSmemBytes = (kAhead + 1) * kIt * kAppThreads * 16;
+  cfg.blockDim = dim3(kPromptThreads);
+  cfg.dynamicSmemBytes = (kAhead + 1) * kPS * kD * 2;
   cfg.stream = st;
-  auto kernel = cache_prompt_kernel<kD, kFmt, kIt, kAhead>;
+  auto kernel = cache_prompt_kernel<kD, kFmt, kPS, kAhead>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute at[1];
@@ -445,18 +466,16 @@ cudaError_t launch_append_t(const CacheGeom& g, const AppendSide& sk, const Appe
                             float* Kbar, cudaStream_t st) {
   // A few tokens for each slot (decode steps, drafts): one CTA a request, no empty clusters to start.
   if (max_tokens <= 4 * (int64_t)g.B) {
-    cache_append_kernel<kD, kFmt><<<dim3((unsigned)g.Hkv, (unsigned)g.B, 2), kAppThreads, 0, st>>>(
+    cache_append_kernel<kD, kFmt><<<dim3((unsigned)g.Hkv, (unsigned)g.B, 2), kStepThreads, 0, st>>>(
         g, sk, sv, max_tokens, cu_new, lens, slots, tables, Kbar);
     return cudaGetLastError();
   }
   auto go = [&](auto fn) { return fn(g, sk, sv, max_tokens, cu_new, lens, slots, tables, Kbar, st); };
-  const int each = g.ps * (kD / 8) / kAppThreads;  // vectors of a page for each thread
-  if constexpr (kD == 128)
-    if (each == 8) return go(launch_prompt<kD, kFmt, 8, 1>);
-  switch (each) {
-    case 4: return go(launch_prompt<kD, kFmt, 4, 2>);
-    case 2: return go(launch_prompt<kD, kFmt, 2, 3>);
-    default: return go(launch_prompt<kD, kFmt, 1, 5>);
+  switch (g.ps) {  // 24 to 64 KB of shared memory: 3 or more CTAs on an SM
+    case 16: return go(launch_prompt<kD, kFmt, 16, 5>);
+    case 32: return go(launch_prompt<kD, kFmt, 32, 3>);
+    case 64: return go(launch_prompt<kD, kFmt, 64, 2>);
+    default: return go(launch_prompt<kD, kFmt, 128, 1>);
   }
 }
 
