@@ -38,33 +38,57 @@ __device__ constexpr float qmax_of() {
 // Least number of 8 significant bits that takes magnitude a to the largest code.
 template <int kFmt>
 __device__ __forceinline__ float scale_for(float a) {
+  constexpr float qmax = qmax_of<kFmt>();
   a = fmaxf(a, kTiny);
-  const uint32_t down = __float_as_uint(__fdiv_rn(a, qmax_of<kFmt>())) & 0xffff0000u;
-  // 8 bits times at most 7 bits: the product is exact
-  return __uint_as_float(__uint_as_float(down) * qmax_of<kFmt>() < a ? down + 0x10000u : down);
+  // a first guess, at most one step off; 8 bits times at most 7 bits: the products are exact
+  uint32_t c = __float_as_uint(a * (1.f / qmax)) & 0xffff0000u;
+  if (__uint_as_float(c) * qmax < a) c += 0x10000u;
+  if (__uint_as_float(c - 0x10000u) * qmax >= a) c -= 0x10000u;
+  return __uint_as_float(c);
 }
 
-// x / s for x and s of 8 significant bits, given inv = rn(1 / s), close enough to be rounded to a
-// code: x * inv is within 2^-23 of the quotient (two roundings of 2^-24); rounding it to 20 bits
-// gives back a quotient that lies half-way between codes (at most 9 bits) exactly, and moves any
-// other by less than the 2^-17 that separate it from there.  Finite x only.  Three operations where
-// a division takes about ten.
-__device__ __forceinline__ float snapped_quotient(float x, float inv) {
-  return __uint_as_float((__float_as_uint(x * inv) + 8u) & ~15u);
+// Quotients x / s for x and s of 8 significant bits, close enough to be rounded to a code.  `up` is
+// 1 / s raised by 2^-21 (and off by at most 2^-23, the reciprocal's own error), so the product lies
+// above the quotient by less than 2^-20 of it, and cutting it to 19 bits (steps of 2^-18) gives back
+// a quotient that lies half-way between codes (at most 9 bits) exactly, while any other stays on its
+// side of the half-way points, from which 2^-17 separate it.  Finite x only.  Half a multiplication
+// (two at a time) and one logic operation each, where a division takes about ten.
+__device__ __forceinline__ float raised_reciprocal(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return r * (1.f + 0x1p-21f);
+}
+__device__ __forceinline__ float2 quotients(float x, float y, float up) {
+  mul2(x, y, x, y, up, up);
+  return make_float2(__uint_as_float(__float_as_uint(x) & ~31u), __uint_as_float(__float_as_uint(y) & ~31u));
 }
 
-// Four values as codes.  kClean: no infinity or NaN among them, and magnitudes up to the largest code.
+// Four values as codes.  kClean: finite, with magnitudes up to the largest code.
 template <int kFmt, bool kClean>
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
-  if constexpr (kFmt == MOBA_CACHE_INT8 && kClean) {
+__device__ __forceinline__ uint32_t codes4(float2 a, float2 b) {
+  if constexpr (kFmt == MOBA_CACHE_E4M3) {
+    uint32_t r;
+    asm("{.reg .b16 l, h;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+        "mov.b32 %0, {l, h};}" : "=r"(r) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+  } else if constexpr (kClean) {
     // adding 1.5 * 2^23 rounds to an integer, ties to even, and leaves it in the low byte
     constexpr float kMagic = 12582912.f;
-    const uint32_t lo = __byte_perm(__float_as_uint(a + kMagic), __float_as_uint(b + kMagic), 0x0040);
-    const uint32_t hi = __byte_perm(__float_as_uint(c + kMagic), __float_as_uint(d + kMagic), 0x0040);
-    return __byte_perm(lo, hi, 0x5410);
+    add2(a.x, a.y, a.x, a.y, kMagic, kMagic);
+    add2(b.x, b.y, b.x, b.y, kMagic, kMagic);
+    return __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
+                       __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
   } else {
-    return float2_to_codes2<kFmt>(a, b) | float2_to_codes2<kFmt>(c, d) << 16;
+    return float2_to_codes2<kFmt>(a.x, a.y) | float2_to_codes2<kFmt>(b.x, b.y) << 16;
   }
+}
+
+// The larger magnitude of each half; NaN stays (signs are left to the caller).
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("{.reg .b32 x, y;\n\tabs.bf16x2 x, %1;\n\tabs.bf16x2 y, %2;\n\tmax.NaN.bf16x2 %0, x, y;}" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 __device__ __forceinline__ float2 bf16x2_to_float2(uint32_t x) {
@@ -73,26 +97,38 @@ __device__ __forceinline__ float2 bf16x2_to_float2(uint32_t x) {
 
 // Eight values over the scale as codes; a page with an infinity or NaN (not kClean) is divided plainly.
 template <int kFmt, bool kClean>
-__device__ __forceinline__ uint2 quantise8(const uint4& x, float scale, float inv) {
-  auto q = [&](float v) { return kClean ? snapped_quotient(v, inv) : __fdiv_rn(v, scale); };
-  const float2 a = bf16x2_to_float2(x.x), b = bf16x2_to_float2(x.y), c = bf16x2_to_float2(x.z), d = bf16x2_to_float2(x.w);
-  return make_uint2(codes4<kFmt, kClean>(q(a.x), q(a.y), q(b.x), q(b.y)),
-                    codes4<kFmt, kClean>(q(c.x), q(c.y), q(d.x), q(d.y)));
+__device__ __forceinline__ uint2 quantise8(const uint4& x, float scale, float up) {
+  auto q = [&](uint32_t w) {
+    const float2 f = bf16x2_to_float2(w);
+    return kClean ? quotients(f.x, f.y, up) : make_float2(__fdiv_rn(f.x, scale), __fdiv_rn(f.y, scale));
+  };
+  return make_uint2(codes4<kFmt, kClean>(q(x.x), q(x.y)), codes4<kFmt, kClean>(q(x.z), q(x.w)));
 }
 
-// Eight codes added to eight sums.
-template <int kFmt>
-__device__ __forceinline__ void add_codes8(float (&sum)[8], const uint2& c) {
-  const uint32_t w[2] = {c.x, c.y};
+// Sums of codes in the thread's kN columns: exact for int8, in fp32 for e4m3.
+template <int kFmt, int kN>
+struct CodeSums {
+  float f[kFmt == MOBA_CACHE_E4M3 ? kN : 1];
+  int i[kFmt == MOBA_CACHE_INT8 ? kN : 1];
+
+  __device__ __forceinline__ CodeSums() : f{}, i{} {}
+  // columns [kAt, kAt + 4)
+  template <int kAt>
+  __device__ __forceinline__ void add4(uint32_t c) {
+    if constexpr (kFmt == MOBA_CACHE_E4M3) {
+      asm("{.reg .b16 l, h, e, o;\n\t.reg .b32 p;\n\tmov.b32 {l, h}, %4;\n\t"
+          "cvt.rn.f16x2.e4m3x2 p, l;\n\tmov.b32 {e, o}, p;\n\tadd.f32.f16 %0, e, %0;\n\tadd.f32.f16 %1, o, %1;\n\t"
+          "cvt.rn.f16x2.e4m3x2 p, h;\n\tmov.b32 {e, o}, p;\n\tadd.f32.f16 %2, e, %2;\n\tadd.f32.f16 %3, o, %3;}"
+          : "+f"(f[kAt]), "+f"(f[kAt + 1]), "+f"(f[kAt + 2]), "+f"(f[kAt + 3]) : "r"(c));
+    } else {
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const float2 lo = codes2_to_float2<kFmt>(w[e]), hi = codes2_to_float2<kFmt>(w[e] >> 16);
-    sum[4 * e] += lo.x;
-    sum[4 * e + 1] += lo.y;
-    sum[4 * e + 2] += hi.x;
-    sum[4 * e + 3] += hi.y;
+      for (int e = 0; e < 4; ++e) i[kAt + e] = __dp4a((int)c, 1 << 8 * e, i[kAt + e]);
+    }
   }
-}
+  __device__ __forceinline__ float sum(int e) const {
+    if constexpr (kFmt == MOBA_CACHE_E4M3) return f[e]; else return (float)i[e];
+  }
+};
 
 // Largest magnitude (bf16 bits) over the block; red holds one value a warp and is used by one call
 // out of two, so that one barrier a call is enough.
@@ -126,11 +162,17 @@ struct PageRows {
   static __device__ __forceinline__ void prefetch(uint32_t stage, const __nv_bfloat16* __restrict__ src, int64_t stride,
                                                   int nr) {
     const int v = threadIdx.x % kVec, r = threadIdx.x / kVec;
+    const __nv_bfloat16* p = src + (int64_t)r * stride + v * 8;
+    stage += threadIdx.x * 16;
+    if (nr == kIt * kRows) {
 #pragma unroll
-    for (int it = 0; it < kIt; ++it) {
-      const bool live = r + it * kRows < nr;
-      cp_async_16(stage + (it * kThreads + threadIdx.x) * 16,
-                  src + (live ? (int64_t)(r + it * kRows) * stride + v * 8 : 0), live ? 16 : 0);
+      for (int it = 0; it < kIt; ++it, p += kRows * stride) cp_async_16(stage + it * kThreads * 16, p, 16);
+    } else {
+#pragma unroll
+      for (int it = 0; it < kIt; ++it, p += kRows * stride) {
+        const bool live = r + it * kRows < nr;
+        cp_async_16(stage + it * kThreads * 16, live ? p : src, live ? 16 : 0);
+      }
     }
   }
   __device__ __forceinline__ void take(uint32_t stage) {
@@ -148,18 +190,34 @@ struct PageRows {
     }
   }
 
+  // kFull: every row of the page, at offset 0.
+  template <bool kPool, bool kClean, bool kFull>
+  __device__ __forceinline__ void write(int nr, uint8_t* dst, float scale, CodeSums<kFmt, 8>& sum) {
+    const float up = raised_reciprocal(scale);
+    uint2* out = reinterpret_cast<uint2*>(dst) + threadIdx.x;  // rows are kVec vectors apart
+#pragma unroll
+    for (int it = 0; it < kIt; ++it)
+      if (kFull || (int)threadIdx.x / kVec + it * kRows < nr) {
+        const uint2 c = quantise8<kFmt, kClean>(x[it], scale, up);
+        out[it * kThreads] = c;
+        if constexpr (kPool) {
+          sum.template add4<0>(c.x);
+          sum.template add4<4>(c.y);
+        }
+      }
+  }
+
   // Into rows [off, off + nr) of the slab.  kPool: sum += codes of the new rows.  Returns the scale.
   template <bool kPool>
   __device__ __forceinline__ float store(int nr, int off, uint8_t* slab, float* scale_ptr, uint32_t (*red)[kMaxWarps],
-                                         int& turn, float (&sum)[8]) {
-    const int v = threadIdx.x % kVec, r = threadIdx.x / kVec;
+                                         int& turn, CodeSums<kFmt, 8>& sum) {
     uint32_t big2 = 0;  // two magnitudes side by side
 #pragma unroll
     for (int it = 0; it < kIt; ++it) {
-      const uint32_t a = __vmaxu2(x[it].x & 0x7fff7fffu, x[it].y & 0x7fff7fffu);
-      const uint32_t b = __vmaxu2(x[it].z & 0x7fff7fffu, x[it].w & 0x7fff7fffu);
-      big2 = __vmaxu2(big2, __vmaxu2(a, b));
+      big2 = max_abs_bf16x2(max_abs_bf16x2(big2, x[it].x), x[it].y);
+      big2 = max_abs_bf16x2(max_abs_bf16x2(big2, x[it].z), x[it].w);
     }
+    big2 &= 0x7fff7fffu;
     uint32_t big = block_max<kThreads>(max(big2 & 0xffffu, big2 >> 16), red[turn ^= 1]);
     const bool clean = big < kInfBits;
     if (!clean) {  // the scale is that of the finite values
@@ -190,22 +248,18 @@ struct PageRows {
           for (int e = 0; e < 2; ++e) {
             const float2 lo = codes2_to_float2<kFmt>(in[e]), hi = codes2_to_float2<kFmt>(in[e] >> 16);
             // the product is exact (at most 15 bits), the quotient as close as one of 8-bit numbers needs
-            out[e] = codes4<kFmt, false>(__fdiv_rn(lo.x * old, scale), __fdiv_rn(lo.y * old, scale),
-                                         __fdiv_rn(hi.x * old, scale), __fdiv_rn(hi.y * old, scale));
+            out[e] = codes4<kFmt, false>(make_float2(__fdiv_rn(lo.x * old, scale), __fdiv_rn(lo.y * old, scale)),
+                                         make_float2(__fdiv_rn(hi.x * old, scale), __fdiv_rn(hi.y * old, scale)));
           }
           rows[i] = make_uint2(out[0], out[1]);
         }
       }
     }
     if (threadIdx.x == 0) *scale_ptr = scale;
-    const float inv = __frcp_rn(scale);
-#pragma unroll
-    for (int it = 0; it < kIt; ++it)
-      if (r + it * kRows < nr) {
-        const uint2 c = clean ? quantise8<kFmt, true>(x[it], scale, inv) : quantise8<kFmt, false>(x[it], scale, inv);
-        reinterpret_cast<uint2*>(slab + (size_t)(off + r + it * kRows) * kD)[v] = c;
-        if constexpr (kPool) add_codes8<kFmt>(sum, c);
-      }
+    uint8_t* dst = slab + (size_t)off * kD;
+    if (!clean) write<kPool, false, false>(nr, dst, scale, sum);
+    else if (nr == kIt * kRows) write<kPool, true, true>(nr, dst, scale, sum);
+    else write<kPool, true, false>(nr, dst, scale, sum);
     return scale;
   }
 };
@@ -214,12 +268,15 @@ struct PageRows {
 template <int kD, int kFmt, int kThreads>
 __device__ __forceinline__ void add_stored_page(const CacheGeom& g, const uint8_t* slab, float scale, float (&acc)[8]) {
   constexpr int kVec = kD / 8, kRows = kThreads / kVec;
-  float sum[8] = {};
+  CodeSums<kFmt, 8> sum;
 #pragma unroll 8
-  for (int r = threadIdx.x / kVec; r < g.ps; r += kRows)
-    add_codes8<kFmt>(sum, reinterpret_cast<const uint2*>(slab + (size_t)r * kD)[threadIdx.x % kVec]);
+  for (int r = threadIdx.x / kVec; r < g.ps; r += kRows) {
+    const uint2 c = reinterpret_cast<const uint2*>(slab + (size_t)r * kD)[threadIdx.x % kVec];
+    sum.template add4<0>(c.x);
+    sum.template add4<4>(c.y);
+  }
 #pragma unroll
-  for (int e = 0; e < 8; ++e) acc[e] = fmaf(sum[e], scale, acc[e]);
+  for (int e = 0; e < 8; ++e) acc[e] = fmaf(sum.sum(e), scale, acc[e]);
 }
 
 // The CTA's sums of its columns (kN of them in each lane): part[d] for all d < kD, visible after the
@@ -286,7 +343,7 @@ __global__ void __launch_bounds__(kStepThreads)
     const int32_t t = t0 + (pos - start), page = page_of_slot(g, slots, t, off);
     if (page >= 0) {
       PageRows<kD, kFmt, 128 * kD / 8 / kStepThreads, kStepThreads> rows;  // any page size
-      float unused[8];
+      CodeSums<kFmt, 8> unused;
       rows.load(a.src + (size_t)head * kD + (int64_t)t * a.stride, a.stride, nr);
       rows.template store<false>(nr, off, a.codes + slab_offset(g, page, head), a.scales + (size_t)page * g.Hkv + head,
                                  sm.red, turn, unused);
@@ -308,15 +365,17 @@ __global__ void __launch_bounds__(kStepThreads)
       }
       const float scale = a.scales[(size_t)page * g.Hkv + head];
       const uint4* src = reinterpret_cast<const uint4*>(a.codes + slab_offset(g, page, head)) + v;
-      float sum[2][8] = {};
+      CodeSums<kFmt, 16> sum;
 #pragma unroll 8
       for (int r = r0; r < g.ps; r += kRows) {
         const uint4 c = src[r * kVec];
-        add_codes8<kFmt>(sum[0], make_uint2(c.x, c.y));
-        add_codes8<kFmt>(sum[1], make_uint2(c.z, c.w));
+        sum.template add4<0>(c.x);
+        sum.template add4<4>(c.y);
+        sum.template add4<8>(c.z);
+        sum.template add4<12>(c.w);
       }
 #pragma unroll
-      for (int e = 0; e < 16; ++e) acc[e] = fmaf(sum[e >> 3][e & 7], scale, acc[e]);
+      for (int e = 0; e < 16; ++e) acc[e] = fmaf(sum.sum(e), scale, acc[e]);
     }
     fold_columns<kD, 16, kStepThreads>(acc, sm);
     if (threadIdx.x < kD)
@@ -406,12 +465,12 @@ __global__ void __launch_bounds__(kPromptThreads, kPS == 128 ? 3 : 4)
     float* sp = a.scales + (size_t)max(page, 0) * g.Hkv + head;
     uint8_t* slab = a.codes + slab_offset(g, max(page, 0), head);
     if (pool && page >= 0 && page == listed && off == 0) {
-      float sum[8] = {};
+      CodeSums<kFmt, 8> sum;
       const float scale = rows.template store<true>(nr, off, slab, sp, sm.red, turn, sum);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = fmaf(sum[e], scale, acc[e]);
+      for (int e = 0; e < 8; ++e) acc[e] = fmaf(sum.sum(e), scale, acc[e]);
     } else {
-      float unused[8];
+      CodeSums<kFmt, 8> unused;
       if (page >= 0) rows.template store<false>(nr, off, slab, sp, sm.red, turn, unused);
       if (pool) {  // older rows are in the page: read all of it back
         __syncthreads();
