@@ -25,7 +25,7 @@
 namespace moba {
 namespace {
 
-constexpr int kStepThreads = 256, kPromptThreads = 128;  // of the two kernels
+constexpr int kStepThreads = 256;  // of cache_append_kernel
 constexpr int kMaxWarps = kStepThreads / 32;
 constexpr float kTiny = 0x1p-96f;  // keeps scales and quotients far from the subnormal range
 constexpr uint32_t kInfBits = 0x7f80;  // magnitude bits of a bf16 infinity; NaN lies above
@@ -401,13 +401,15 @@ __device__ __forceinline__ int request_of_item(const CacheGeom& g, const int32_t
   return lo;
 }
 
+__host__ __device__ constexpr int prompt_threads(int ps) { return ps == 128 ? 256 : 128; }
+
 // kPS: tokens of a page; kAhead: pages on their way while one is written.
 template <int kD, int kFmt, int kPS, int kAhead>
-__global__ void __launch_bounds__(kPromptThreads, kPS == 128 ? 3 : 4)
+__global__ void __launch_bounds__(prompt_threads(kPS), kPS == 128 ? 3 : 6)
     cache_prompt_kernel(CacheGeom g, AppendSide sk, AppendSide sv, int32_t max_tokens, int ranks,
                         const int32_t* __restrict__ cu_new, const int32_t* __restrict__ lens,
                         const int32_t* __restrict__ slots, const int32_t* __restrict__ tables, float* Kbar) {
-  constexpr int kIt = kPS * (kD / 8) / kPromptThreads;
+  constexpr int kPromptThreads = prompt_threads(kPS), kIt = kPS * (kD / 8) / kPromptThreads;
   using Rows = PageRows<kD, kFmt, kIt, kPromptThreads>;
   constexpr uint32_t kStageBytes = kIt * kPromptThreads * 16;
   g.ps = kPS;
@@ -503,7 +505,7 @@ cudaError_t launch_prompt(const CacheGeom& g, const AppendSide& sk, const Append
   const int64_t items = max_tokens / g.bs + 2 * (int64_t)g.B;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(items * ranks), (unsigned)g.Hkv, 2);
-  cfg.blockDim = dim3(kPromptThreads);
+  cfg.blockDim = dim3(prompt_threads(kPS));
   cfg.dynamicSmemBytes = (kAhead + 1) * kPS * kD * 2;
   cfg.stream = st;
   auto kernel = cache_prompt_kernel<kD, kFmt, kPS, kAhead>;
@@ -531,9 +533,9 @@ cudaError_t launch_append_t(const CacheGeom& g, const AppendSide& sk, const Appe
   }
   auto go = [&](auto fn) { return fn(g, sk, sv, max_tokens, cu_new, lens, slots, tables, Kbar, st); };
   switch (g.ps) {  // 24 to 64 KB of shared memory: 3 or more CTAs on an SM
-    case 16: return go(launch_prompt<kD, kFmt, 16, 5>);
-    case 32: return go(launch_prompt<kD, kFmt, 32, 3>);
-    case 64: return go(launch_prompt<kD, kFmt, 64, 2>);
+    case 16: return go(launch_prompt<kD, kFmt, 16, 4>);
+    case 32: return go(launch_prompt<kD, kFmt, 32, 2>);
+    case 64: return go(launch_prompt<kD, kFmt, 64, 1>);
     default: return go(launch_prompt<kD, kFmt, 128, 1>);
   }
 }
