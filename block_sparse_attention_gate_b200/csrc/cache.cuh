@@ -79,9 +79,10 @@ struct __align__(16) CacheSeg {
 // Work space of one decode call (device pointers), and how its blocks are cut.  An entry of the work
 // list is a (request, KV head, tile of 8 heads), its units are chunks of CK keys.
 struct CacheDecodeWork {
-  double* score;     // [B, Hq, MB] gate scores
+  uint64_t* score;   // [B, Hq, MB] gate scores, as ordered keys
   CacheSeg* segs;    // [entries, max_segs] distinct blocks, the own one first
   int32_t* units;    // [entries] chunks in all
+  int32_t* arrived;  // [B, Hq] partial results that are there
   float* part_o;     // [B, Hq, k, NC, D] partial sums of weighted values
   float2* part_ml;   // [B, Hq, k, NC] running maximum (log2 units), sum of the softmax
   int32_t* sel;      // [B, Hq, k] (used when the caller passes none)

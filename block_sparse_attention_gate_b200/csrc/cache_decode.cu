@@ -4,11 +4,12 @@
 //   z_j = scale * <q, code_j> * Ks[page(j)],  O = sum_j softmax(z)_j * code'_j * Vs[page(j)],
 //   LSE = log sum_j exp(z_j).   A request of length 0 gets O = 0, LSE = -inf, no blocks.
 //
-//   cache_gate_kernel : scores and choice of every head of a (request, KV head), and the list of
-//                       the distinct blocks that those heads chose.
-//   cache_attn_kernel : each distinct block is read once for all the heads (up to 8) that chose
-//                       it, in chunks of CK keys spread evenly over the warps of a persistent grid.
-//   cache_merge_kernel: the chunks' partial results of a (request, head), by online softmax.
+//   cache_gate_kernel: scores and choice of every head of a (request, KV head), and the list of the
+//                      distinct blocks that those heads chose.
+//   cache_attn_kernel: each distinct block is read once for all the heads (up to 8) that chose it, in
+//                      chunks of CK keys spread evenly over the warps of a persistent grid.  The warp
+//                      that finishes a (request, head) merges its chunks' partial results, always in
+//                      the same order: a row's result does not depend on the other requests.
 //
 // Bound by HBM: the chosen blocks' codes, 2 D bytes a key and KV head.
 #include <cudaTypedefs.h>
@@ -28,38 +29,58 @@ constexpr float kLn2C = 0.6931471805599453f;
 // there): the choice is that of the exact scores but for ties to about 2^-50.
 
 constexpr int kGateWarps = 8;
+constexpr int kGateRows = 8;   // blocks that a warp scores at a time
+constexpr int kHeld = 8;       // scores that a lane holds while a head's best are picked
 
-__device__ __forceinline__ bool ranks_before(double sa, int32_t ba, double sb, int32_t bb) {
-  return sa > sb || (sa == sb && ba < bb);
+// Order of scores as unsigned numbers: NaN last, -0 as +0.  No score maps to 0.
+__device__ __forceinline__ uint64_t score_key(double x) {
+  x = x == x ? x + 0.0 : -INFINITY;
+  const uint64_t u = (uint64_t)__double_as_longlong(x);
+  return u >> 63 ? ~u : u | 1ull << 63;
 }
 
-// Sum of v[x] over the warp's lanes, for all 32 x at once: lane x returns the sum of v[x].  Each
-// step halves the values a lane still carries: 31 exchanges instead of 5 for every value.
-__device__ __forceinline__ double warp_sums(double (&v)[32]) {
+// Sums of kN values over the warp's lanes, all at once: lane x returns the sum of v[x / (32 / kN)].
+// Each of the first steps halves the values that a lane still carries.
+template <int kN>
+__device__ __forceinline__ double warp_sums(double (&v)[kN]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int half = 16; half >= 1; half >>= 1) {
-    const bool up = (lane & half) != 0;
+  for (int off = 16; off >= 1; off >>= 1) {
+    const int half = kN * off / 32;  // values left after this step
+    if (half >= 1) {
+      const bool up = (lane & off) != 0;
 #pragma unroll
-    for (int x = 0; x < half; ++x) {
-      const double give = up ? v[x] : v[x + half], keep = up ? v[x + half] : v[x];
-      v[x] = keep + __shfl_xor_sync(0xffffffffu, give, half);
+      for (int x = 0; x < half; ++x) {
+        const double give = up ? v[x] : v[x + half], keep = up ? v[x + half] : v[x];
+        v[x] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+      }
+    } else {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
     }
   }
   return v[0];
 }
 
-// The cluster of a (request, KV head): its CTAs share the earlier blocks' scores (kH heads and
-// 32 / kH blocks a warp at a time, a lane per D / 32 dimensions), then CTA 0 chooses, a warp a
-// head, and lists the distinct blocks of every 8 heads.
+// The best key of the lanes' best (key, block), ties to the lower block; the block that has it.
+__device__ __forceinline__ int32_t warp_best(uint64_t key, int32_t b) {
+  const uint32_t hi = (uint32_t)(key >> 32), top = __reduce_max_sync(0xffffffffu, hi);
+  const uint32_t lo = hi == top ? (uint32_t)key : 0u, low = __reduce_max_sync(0xffffffffu, lo);
+  return (int32_t)__reduce_min_sync(0xffffffffu, hi == top && lo == low ? (uint32_t)b : 0xffffffffu);
+}
+
+// The cluster of a (request, KV head): its CTAs share the earlier blocks' scores (kH heads and 8
+// blocks a warp at a time, a lane per D / 32 dimensions), then CTA 0 chooses, a warp a head, and
+// lists the distinct blocks of every 8 heads.
 template <int kD, int kH>
 __global__ void __launch_bounds__(kGateWarps * 32)
     cache_gate_kernel(CacheGeom g, const __nv_bfloat16* __restrict__ Q, const float* __restrict__ Kbar,
-                      const int32_t* __restrict__ lens, int32_t* __restrict__ sel, CacheDecodeWork w) {
-  constexpr int kDL = kD / 32, kR = 32 / kH;
+                      const int32_t* __restrict__ lens, int32_t* __restrict__ sel, CacheDecodeWork w,
+                      __nv_bfloat16* __restrict__ O, float* __restrict__ LSE) {
+  constexpr int kDL = kD / 32;
   __shared__ int32_t s_sel[8][kMaxTopK];
   const int rank = blockIdx.x, gk = blockIdx.y, s = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  launch_dependents();  // the attention kernel may be set up meanwhile
   const int32_t len = cached_len(g, lens, s);
   const int i = len > 0 ? (len - 1) / g.bs : -1;
   const size_t row0 = (size_t)s * g.Hq + (size_t)gk * g.G;
@@ -71,10 +92,10 @@ __global__ void __launch_bounds__(kGateWarps * 32)
 #pragma unroll
         for (int x = 0; x < kDL; ++x)
           q[h][x] = h0 + h < g.G ? (double)__bfloat162float(Q[(row0 + h0 + h) * kD + lane * kDL + x]) : 0.0;
-      for (int b0 = (rank * kGateWarps + warp) * kR; b0 < i; b0 += gridDim.x * kGateWarps * kR) {
-        float kb[kR][kDL];
+      for (int b0 = (rank * kGateWarps + warp) * kGateRows; b0 < i; b0 += gridDim.x * kGateWarps * kGateRows) {
+        float kb[kGateRows][kDL];
 #pragma unroll
-        for (int r = 0; r < kR; ++r) {
+        for (int r = 0; r < kGateRows; ++r) {
           const float* src = Kbar + (((size_t)s * g.MB + b0 + r) * g.Hkv + gk) * kD + lane * kDL;
           if (b0 + r < i) {
             if constexpr (kDL == 4) {
@@ -89,9 +110,9 @@ __global__ void __launch_bounds__(kGateWarps * 32)
             for (int x = 0; x < kDL; ++x) kb[r][x] = 0.f;
           }
         }
-        double v[32];
+        double v[kGateRows * kH];
 #pragma unroll
-        for (int r = 0; r < kR; ++r)
+        for (int r = 0; r < kGateRows; ++r)
 #pragma unroll
           for (int h = 0; h < kH; ++h) {
             double acc = 0.0;
@@ -99,44 +120,62 @@ __global__ void __launch_bounds__(kGateWarps * 32)
             for (int x = 0; x < kDL; ++x) acc = fma(q[h][x], (double)kb[r][x], acc);
             v[r * kH + h] = acc;
           }
-        const double sum = warp_sums(v);
-        const int r = lane / kH, h = lane % kH;
-        if (b0 + r < i && h0 + h < g.G)
-          w.score[(row0 + h0 + h) * g.MB + b0 + r] = sum == sum ? sum : -INFINITY;  // NaN ranks last
+        const uint64_t key = score_key(warp_sums<kGateRows * kH>(v));
+        const int x = lane / (4 / kH), r = x / kH, h = x % kH;
+        if (lane % (4 / kH) == 0 && b0 + r < i && h0 + h < g.G) w.score[(row0 + h0 + h) * g.MB + b0 + r] = key;
       }
     }
     if (gridDim.x > 1) cluster_barrier(); else __syncthreads();
   }
   if (rank != 0) return;
+  if (i < 0) {  // an empty request
+    for (int x = threadIdx.x; x < g.G * kD; x += kGateWarps * 32) O[row0 * kD + x] = __float2bfloat16(0.f);
+    for (int x = threadIdx.x; x < g.G; x += kGateWarps * 32) LSE[row0 + x] = -INFINITY;
+  }
   const int m = min(g.k - 1, max(i, 0)), HT = (g.G + 7) / 8;
   for (int ht = 0; ht < HT; ++ht) {
     const int hh = ht * 8 + warp, heads = min(8, g.G - ht * 8);
     if (hh < g.G) {
-      const double* sc = w.score + (row0 + hh) * g.MB;
+      const uint64_t* sc = w.score + (row0 + hh) * g.MB;
       int32_t mine = lane == 0 ? i : -1;  // this lane's entry of the row of sel
-      double last = INFINITY;
-      int32_t last_b = -1;
-      for (int q = 0; q < m; ++q) {
-        double best = -INFINITY;
-        int32_t bb = INT32_MAX;
-        for (int b = lane; b < i; b += 32) {
-          const double v = sc[b];
-          if (ranks_before(last, last_b, v, b) && ranks_before(v, b, best, bb)) { best = v; bb = b; }
-        }
+      if (i <= kHeld * 32) {
+        uint64_t held[kHeld];
 #pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) {
-          const double os = __shfl_xor_sync(0xffffffffu, best, off);
-          const int32_t ob = __shfl_xor_sync(0xffffffffu, bb, off);
-          if (ranks_before(os, ob, best, bb)) { best = os; bb = ob; }
+        for (int x = 0; x < kHeld; ++x) held[x] = x * 32 + lane < i && m > 0 ? sc[x * 32 + lane] : 0;
+        for (int q = 0; q < m; ++q) {
+          uint64_t best = held[0];
+          int at = 0;
+#pragma unroll
+          for (int x = 1; x < kHeld; ++x)
+            if (held[x] > best) best = held[x], at = x;
+          const int32_t bb = warp_best(best, at * 32 + lane);
+          if (lane == 1 + q) mine = bb;
+#pragma unroll
+          for (int x = 0; x < kHeld; ++x)
+            if (x * 32 + lane == bb) held[x] = 0;
         }
-        if (lane == 1 + q) mine = bb;
-        last = best;
-        last_b = bb;
+      } else {  // too many to hold: each round looks for the best behind the last one
+        uint64_t last = ~0ull;
+        int32_t last_b = -1;
+        for (int q = 0; q < m; ++q) {
+          uint64_t best = 0;
+          int32_t bb = 0;
+#pragma unroll 8
+          for (int b = lane; b < i; b += 32) {
+            const uint64_t v = sc[b];
+            if ((v < last || (v == last && b > last_b)) && v > best) best = v, bb = b;
+          }
+          const int32_t won = warp_best(best, bb);
+          last = __shfl_sync(0xffffffffu, best, won & 31);
+          last_b = won;
+          if (lane == 1 + q) mine = won;
+        }
       }
       if (lane < g.k) {
         sel[(row0 + hh) * g.k + lane] = mine;
         s_sel[warp][lane] = mine;
       }
+      if (lane == 0) w.arrived[row0 + hh] = 0;
     }
     __syncthreads();
     if (warp == 0) {
@@ -151,18 +190,17 @@ __global__ void __launch_bounds__(kGateWarps * 32)
       int count = i >= 0 ? 1 : 0;
       const int n = heads * m;  // chosen (head, slot) pairs, head by head
       for (int e0 = 0; e0 < n; e0 += 32) {
-        const int e = e0 + lane, h = e / max(m, 1);
-        const int32_t b = e < n ? s_sel[h][1 + e % m] : -1;
+        const int e = e0 + lane, eh = e / m, ej = 1 + e - eh * m;
+        const int32_t b = e < n ? s_sel[eh][ej] : -1;
         bool first = e < n;
         CacheSeg seg{b, 0, {~0u, ~0u}};
-        if (e < n)
-          for (int o = 0; o < n; ++o) {
-            const int oh = o / m, oj = 1 + o % m;
-            if (s_sel[oh][oj] == b) {
-              if (o < e) first = false;
-              seg.slots[oh >> 2] &= ~(0xffu << 8 * (oh & 3)) | (uint32_t)oj << 8 * (oh & 3);
+        for (int oh = 0; oh < heads; ++oh)
+          for (int oj = 1; oj <= m; ++oj)
+            if (e < n && s_sel[oh][oj] == b) {
+              if (oh < eh) first = false;  // a head chooses a block once
+              const uint32_t keep = ~(0xffu << 8 * (oh & 3)), put = (uint32_t)oj << 8 * (oh & 3);
+              if (oh < 4) seg.slots[0] = (seg.slots[0] & keep) | put; else seg.slots[1] = (seg.slots[1] & keep) | put;
             }
-          }
         const uint32_t firsts = __ballot_sync(0xffffffffu, first);
         if (first) segs[count + __popc(firsts & ((1u << lane) - 1))] = seg;
         count += __popc(firsts);
@@ -270,6 +308,7 @@ struct Piece {
   int chunk;              // of the block
   int key0, n, left;      // first key in the block, keys here, keys of the unit behind this piece
   uint32_t slots[2];
+  int own_chunks, parts;  // chunks of the request's own block, and of all blocks of one head
   bool begins;            // first piece of its unit
 };
 
@@ -280,12 +319,14 @@ __device__ __forceinline__ void open_unit(const CacheGeom& g, const CacheDecodeW
   p.gk = sg % g.Hkv;
   p.s = sg / g.Hkv;
   const int32_t len = cached_len(g, lens, p.s);
-  const int own = (len - 1) / g.bs, own_n = len - own * g.bs, own_chunks = (own_n + w.CK - 1) / w.CK;
+  const int own = (len - 1) / g.bs, own_n = len - own * g.bs;
+  p.own_chunks = (own_n + w.CK - 1) / w.CK;
+  p.parts = p.own_chunks + min(g.k - 1, own) * w.NC;
   int seg = 0, bn = own_n;
   p.chunk = p.unit;
-  if (p.unit >= own_chunks) {
-    seg = 1 + (p.unit - own_chunks) / w.NC;
-    p.chunk = (p.unit - own_chunks) % w.NC;
+  if (p.unit >= p.own_chunks) {
+    seg = 1 + (p.unit - p.own_chunks) / w.NC;
+    p.chunk = (p.unit - p.own_chunks) % w.NC;
     bn = g.bs;
   }
   const int4 e = __ldg(reinterpret_cast<const int4*>(w.segs + (size_t)p.idx * w.max_segs + seg));
@@ -299,11 +340,77 @@ __device__ __forceinline__ void open_unit(const CacheGeom& g, const CacheDecodeW
   p.begins = true;
 }
 
+// Adds 1; what the warp wrote before (and synchronised) is seen by whoever sees the new value.
+__device__ __forceinline__ int atomic_inc_acq_rel(int32_t* p) {
+  int old;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(p) : "memory");
+  return old;
+}
+
+// The partial results of one (request, head), merged by online softmax (log2 units) by one warp.
+template <int kD>
+__device__ __forceinline__ void merge_row(const CacheGeom& g, const CacheDecodeWork& w, size_t row, int own_chunks, int n,
+                                          __nv_bfloat16* __restrict__ O, float* __restrict__ LSE) {
+  constexpr int kDL = kD / 32;
+  const int lane = threadIdx.x & 31;
+  const float2* ml = w.part_ml + row * g.k * w.NC;
+  const float* po = w.part_o + row * g.k * w.NC * kD + lane * kDL;
+  auto at = [&](int x) { return x < own_chunks ? x : w.NC + (x - own_chunks); };
+  float M = -INFINITY;
+  float2 held = make_float2(-INFINITY, 0.f);  // of part `lane`
+  if (lane < n) held = __ldcg(&ml[at(lane)]);
+  M = held.x;
+  for (int x = 32 + lane; x < n; x += 32) M = fmaxf(M, __ldcg(&ml[at(x)]).x);
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  const float base = M == -INFINITY ? 0.f : M;
+  float L = 0.f, acc[kDL];
+#pragma unroll
+  for (int d = 0; d < kDL; ++d) acc[d] = 0.f;
+  for (int x0 = 0; x0 < n; x0 += 32) {
+    if (x0 > 0) {
+      held = make_float2(-INFINITY, 0.f);
+      if (x0 + lane < n) held = __ldcg(&ml[at(x0 + lane)]);
+    }
+    const float wt = ex2(held.x - base);  // 0 behind the last part
+    L = fmaf(held.y, wt, L);
+    for (int x1 = x0; x1 < min(n, x0 + 32); x1 += 16) {  // 16 rows on their way at a time
+      float f[16][kDL];
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        const float* src = po + (size_t)at(min(x1 + x, n - 1)) * kD;
+        if constexpr (kDL == 4) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+          f[x][0] = v.x, f[x][1] = v.y, f[x][2] = v.z, f[x][3] = v.w;
+        } else {
+          const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+          f[x][0] = v.x, f[x][1] = v.y;
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        const float wx = __shfl_sync(0xffffffffu, wt, (x1 + x) & 31);
+        if (x1 + x < n)
+#pragma unroll
+          for (int d = 0; d < kDL; ++d) acc[d] = fmaf(wx, f[x][d], acc[d]);
+      }
+    }
+  }
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+  const float inv = L == 0.f ? 0.f : 1.f / L;  // 0: no key at all
+#pragma unroll
+  for (int d = 0; d < kDL; d += 2)
+    *reinterpret_cast<__nv_bfloat162*>(O + row * kD + lane * kDL + d) = __floats2bfloat162_rn(acc[d] * inv, acc[d + 1] * inv);
+  if (lane == 0) LSE[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2C;
+}
+
 template <int kD, int kFmt>
 __global__ void __launch_bounds__(kAttnWarps * 32, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, CacheGeom g,
                       const __nv_bfloat16* __restrict__ Q, const float* __restrict__ Ks, const float* __restrict__ Vs,
-                      const int32_t* __restrict__ lens, const int32_t* __restrict__ tables, CacheDecodeWork w, int NI) {
+                      const int32_t* __restrict__ lens, const int32_t* __restrict__ tables, CacheDecodeWork w, int NI,
+                      __nv_bfloat16* __restrict__ O, float* __restrict__ LSE) {
   using L = AttnLayout<kD>;
   constexpr int kW = kD / 16;   // k steps of K Q^T = 16-row tiles of V^T
   extern __shared__ uint8_t smem_raw[];
@@ -313,6 +420,14 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar) + warp * kStages;
   int32_t* prefix = reinterpret_cast<int32_t*>(smem + L::kPrefix);
   int32_t* wsum = prefix + L::kMaxPrefix + 1;
+
+  if (lane == 0) {
+    for (int q = 0; q < kStages; ++q) mbar_init(&full[q], 1);
+    fence_mbar_init();
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+  }
+  wait_for_primary();  // the gate's results
 
   // ---- units before each group of `per` entries of the work list
   const int per = (NI + L::kMaxPrefix - 1) / L::kMaxPrefix, groups = (NI + per - 1) / per;
@@ -333,10 +448,6 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1)
     if (lane >= off) inc += o;
   }
   if (lane == 31) wsum[warp] = inc;
-  if (lane == 0) {
-    for (int q = 0; q < kStages; ++q) mbar_init(&full[q], 1);
-    fence_mbar_init();
-  }
   __syncthreads();
   int32_t before = inc - sum;
   for (int q = 0; q < warp; ++q) before += wsum[q];
@@ -611,6 +722,14 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1)
           if (gq == 0) w.part_ml[part] = make_float2(m[e], ls[e]);
         }
       }
+      // whoever brings a row's last part merges it (the gate has set the counters to 0)
+      __syncwarp();
+      const size_t row0 = (size_t)cur.s * g.Hq + (size_t)cur.gk * g.G + cur.ht * 8;
+      bool last = false;
+      if (lane < 8 && (((lane < 4 ? cur.slots[0] : cur.slots[1]) >> 8 * (lane & 3)) & 0xffu) != 0xffu)
+        last = atomic_inc_acq_rel(w.arrived + row0 + lane) == cur.parts - 1;
+      uint32_t rows = __ballot_sync(0xffffffffu, last);
+      for (; rows; rows &= rows - 1) merge_row<kD>(g, w, row0 + __ffs(rows) - 1, cur.own_chunks, cur.parts, O, LSE);
     }
     if (!more) break;
     cur = nxt;
@@ -628,65 +747,6 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1)
       mbar_wait_warp(&full[rd], parity, g.err);
       if (++rd == kStages) rd = 0, parity ^= 1;
     }
-}
-
-// The chunks of a (request, head), one warp each row, merged by online softmax (log2 units).
-template <int kD>
-__global__ void __launch_bounds__(128)
-    cache_merge_kernel(CacheGeom g, const int32_t* __restrict__ lens, const int32_t* __restrict__ sel,
-                       CacheDecodeWork w, __nv_bfloat16* __restrict__ O, float* __restrict__ LSE) {
-  constexpr int kDL = kD / 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const size_t row = (size_t)blockIdx.x * 4 + warp;
-  if (row >= (size_t)g.B * g.Hq) return;
-  const int32_t len = cached_len(g, lens, (int)(row / g.Hq));
-  const int own_n = len > 0 ? len - (len - 1) / g.bs * g.bs : 0, own_chunks = (own_n + w.CK - 1) / w.CK;
-  const int32_t my = lane < g.k ? __ldg(sel + row * g.k + lane) : -1;
-  const int slots = __popc(__ballot_sync(0xffffffffu, my >= 0));  // filled from the front
-  const int n = slots ? own_chunks + (slots - 1) * w.NC : 0;
-  const float2* ml = w.part_ml + row * g.k * w.NC;
-  const float* po = w.part_o + row * g.k * w.NC * kD + lane * kDL;
-  auto at = [&](int x) { return x < own_chunks ? x : w.NC + (x - own_chunks); };
-  float M = -INFINITY;
-  for (int x = lane; x < n; x += 32) M = fmaxf(M, ml[at(x)].x);
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  const float base = M == -INFINITY ? 0.f : M;
-  float L = 0.f, acc[kDL];
-#pragma unroll
-  for (int d = 0; d < kDL; ++d) acc[d] = 0.f;
-  for (int x0 = 0; x0 < n; x0 += 32) {
-    float wt = 0.f;
-    if (x0 + lane < n) {
-      const float2 v = ml[at(x0 + lane)];
-      wt = ex2(v.x - base);
-      L = fmaf(v.y, wt, L);
-    }
-    const int c = min(32, n - x0);
-#pragma unroll 8
-    for (int x = 0; x < c; ++x) {
-      const float wx = __shfl_sync(0xffffffffu, wt, x);
-      const float* src = po + (size_t)at(x0 + x) * kD;
-      if constexpr (kDL == 4) {
-        const float4 f = *reinterpret_cast<const float4*>(src);
-        acc[0] = fmaf(wx, f.x, acc[0]);
-        acc[1] = fmaf(wx, f.y, acc[1]);
-        acc[2] = fmaf(wx, f.z, acc[2]);
-        acc[3] = fmaf(wx, f.w, acc[3]);
-      } else {
-        const float2 f = *reinterpret_cast<const float2*>(src);
-        acc[0] = fmaf(wx, f.x, acc[0]);
-        acc[1] = fmaf(wx, f.y, acc[1]);
-      }
-    }
-  }
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-  const float inv = L == 0.f ? 0.f : 1.f / L;  // 0: no key at all
-#pragma unroll
-  for (int d = 0; d < kDL; d += 2)
-    *reinterpret_cast<__nv_bfloat162*>(O + row * kD + lane * kDL + d) = __floats2bfloat162_rn(acc[d] * inv, acc[d + 1] * inv);
-  if (lane == 0) LSE[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2C;
 }
 
 // ---------------------------------------------------------------------------------- launch
@@ -716,10 +776,10 @@ cudaError_t make_codes_map(CUtensorMap* m, const void* base, const CacheGeom& g)
 
 template <int kD, int kH>
 cudaError_t launch_gate(const CacheGeom& g, const __nv_bfloat16* Q, const float* Kbar, const int32_t* lens,
-                        int32_t* sel, const CacheDecodeWork& w, cudaStream_t st) {
-  // CTAs of a cluster share the candidates: 8 warps take 32 / kH blocks each at a time
+                        int32_t* sel, const CacheDecodeWork& w, __nv_bfloat16* O, float* LSE, cudaStream_t st) {
+  // CTAs of a cluster share the candidates, 64 blocks each at a time
   int c = 1;
-  while (c < 8 && g.k > 1 && c * kGateWarps * (32 / kH) < g.MB - 1) c *= 2;
+  while (c < 8 && g.k > 1 && c * kGateWarps * kGateRows < g.MB - 1) c *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)c, (unsigned)g.Hkv, (unsigned)g.B);
   cfg.blockDim = dim3(kGateWarps * 32);
@@ -730,7 +790,7 @@ cudaError_t launch_gate(const CacheGeom& g, const __nv_bfloat16* Q, const float*
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_gate_kernel<kD, kH>, g, Q, Kbar, lens, sel, w);
+  return cudaLaunchKernelEx(&cfg, cache_gate_kernel<kD, kH>, g, Q, Kbar, lens, sel, w, O, LSE);
 }
 
 template <int kD, int kFmt>
@@ -738,9 +798,9 @@ cudaError_t launch_decode_t(const CacheGeom& g, const __nv_bfloat16* Q, const ui
                             const float* Ks, const float* Vs, const float* Kbar, const int32_t* lens,
                             const int32_t* tables, int32_t* sel, const CacheDecodeWork& w, __nv_bfloat16* O,
                             float* LSE, int sms, cudaStream_t st) {
-  cudaError_t e = g.G == 1   ? launch_gate<kD, 1>(g, Q, Kbar, lens, sel, w, st)
-                  : g.G == 2 ? launch_gate<kD, 2>(g, Q, Kbar, lens, sel, w, st)
-                             : launch_gate<kD, 4>(g, Q, Kbar, lens, sel, w, st);
+  cudaError_t e = g.G == 1   ? launch_gate<kD, 1>(g, Q, Kbar, lens, sel, w, O, LSE, st)
+                  : g.G == 2 ? launch_gate<kD, 2>(g, Q, Kbar, lens, sel, w, O, LSE, st)
+                             : launch_gate<kD, 4>(g, Q, Kbar, lens, sel, w, O, LSE, st);
   if (e != cudaSuccess) return e;
   CUtensorMap tk, tv;
   if ((e = make_codes_map(&tk, Kc, g)) != cudaSuccess) return e;
@@ -748,24 +808,34 @@ cudaError_t launch_decode_t(const CacheGeom& g, const __nv_bfloat16* Q, const ui
   auto attn = cache_attn_kernel<kD, kFmt>;
   if ((e = cudaFuncSetAttribute(attn, cudaFuncAttributeMaxDynamicSharedMemorySize, AttnLayout<kD>::kAlloc)) != cudaSuccess)
     return e;
-  const int NI = g.B * g.Hkv * ((g.G + 7) / 8);
-  attn<<<sms, kAttnWarps * 32, AttnLayout<kD>::kAlloc, st>>>(tk, tv, g, Q, Ks, Vs, lens, tables, w, NI);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const size_t rows = (size_t)g.B * g.Hq;
-  cache_merge_kernel<kD><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(g, lens, sel, w, O, LSE);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)sms);
+  cfg.blockDim = dim3(kAttnWarps * 32);
+  cfg.dynamicSmemBytes = AttnLayout<kD>::kAlloc;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];  // its CTAs may start while the gate runs, and wait for its results there
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn, tk, tv, g, Q, Ks, Vs, lens, tables, w, g.B * g.Hkv * ((g.G + 7) / 8), O, LSE);
 }
 
 }  // namespace
 
-// Keys of a unit.  Long chunks write fewer partial rows, short ones spread a small problem over the
-// GPU: the longest that leaves every warp two units if all heads of a group agree, at least 128.
-// A power of two, so that the pieces of every unit start on a page.
+// Keys of a unit, a power of two so that the pieces of every unit start on a page.  Long chunks write
+// and merge fewer partial rows, short ones spread a small problem over the GPU.  Counting the units
+// that there are at the least (all heads of a group agree): the longest chunks that still give every
+// warp two units; a problem too small for that with chunks of 512 takes at most 512, and as many fewer
+// as give every second warp a unit (half of the warps have copies enough in flight to fill the memory).
 int cache_chunk_keys(const CacheGeom& g) {
-  const int64_t rows = (int64_t)g.B * g.Hkv * ((g.G + 7) / 8) * g.k;
-  int ck = 8192;
-  while (ck > 128 && (ck / 2 >= g.bs || rows * ((g.bs + ck - 1) / ck) < 2 * 148 * kAttnWarps)) ck /= 2;
-  return ck;
+  const int64_t rows = (int64_t)g.B * g.Hkv * ((g.G + 7) / 8) * g.k, warps = 148 * kAttnWarps;
+  auto longest = [&](int64_t units, int ck) {
+    while (ck > 128 && (ck / 2 >= g.bs || rows * ((g.bs + ck - 1) / ck) < units)) ck /= 2;
+    return ck;
+  };
+  const int most = longest(2 * warps, 8192);
+  return most >= 512 ? most : longest(warps / 2, 512);
 }
 
 cudaError_t launch_cache_decode(const CacheGeom& g, const __nv_bfloat16* Q, const uint8_t* Kc, const uint8_t* Vc,
