@@ -82,7 +82,6 @@ struct CacheDecodeWork {
   uint64_t* score;   // [B, Hq, MB] gate scores, as ordered keys
   CacheSeg* segs;    // [entries, max_segs] distinct blocks, the own one first
   int32_t* units;    // [entries] chunks in all
-  int32_t* arrived;  // [B, Hq] partial results that are there
   float* part_o;     // [B, Hq, k, NC, D] partial sums of weighted values
   float2* part_ml;   // [B, Hq, k, NC] running maximum (log2 units), sum of the softmax
   int32_t* sel;      // [B, Hq, k] (used when the caller passes none)

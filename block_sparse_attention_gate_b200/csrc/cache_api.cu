@@ -108,7 +108,6 @@ moba::CacheDecodeWork carve_cache_decode(const moba::CacheGeom& g, char* base) {
   w.score = (uint64_t*)take(g.k > 1 ? rows * g.MB * sizeof(uint64_t) : 0);
   w.segs = (moba::CacheSeg*)take(entries * w.max_segs * sizeof(moba::CacheSeg));
   w.units = (int32_t*)take(entries * sizeof(int32_t));
-  w.arrived = (int32_t*)take(rows * sizeof(int32_t));
   w.part_o = (float*)take(parts * g.D * sizeof(float));
   w.part_ml = (float2*)take(parts * sizeof(float2));
   w.sel = (int32_t*)take(rows * g.k * sizeof(int32_t));

@@ -7,9 +7,9 @@
 //   cache_gate_kernel: scores and choice of every head of a (request, KV head), and the list of the
 //                      distinct blocks that those heads chose.
 //   cache_attn_kernel: each distinct block is read once for all the heads (up to 8) that chose it, in
-//                      chunks of CK keys spread evenly over the warps of a persistent grid.  The warp
-//                      that finishes a (request, head) merges its chunks' partial results, always in
-//                      the same order: a row's result does not depend on the other requests.
+//                      chunks of CK keys spread evenly over the warps of a persistent grid.
+//   cache_merge_kernel: the chunks' partial results of a (request, head), by online softmax, always
+//                      cut and added up in the same order: a row does not depend on other requests.
 //
 // Bound by HBM: the chosen blocks' codes, 2 D bytes a key and KV head.
 #include <cudaTypedefs.h>
@@ -74,8 +74,7 @@ __device__ __forceinline__ int32_t warp_best(uint64_t key, int32_t b) {
 template <int kD, int kH>
 __global__ void __launch_bounds__(kGateWarps * 32)
     cache_gate_kernel(CacheGeom g, const __nv_bfloat16* __restrict__ Q, const float* __restrict__ Kbar,
-                      const int32_t* __restrict__ lens, int32_t* __restrict__ sel, CacheDecodeWork w,
-                      __nv_bfloat16* __restrict__ O, float* __restrict__ LSE) {
+                      const int32_t* __restrict__ lens, int32_t* __restrict__ sel, CacheDecodeWork w) {
   constexpr int kDL = kD / 32;
   __shared__ int32_t s_sel[8][kMaxTopK];
   const int rank = blockIdx.x, gk = blockIdx.y, s = blockIdx.z;
@@ -128,10 +127,6 @@ __global__ void __launch_bounds__(kGateWarps * 32)
     if (gridDim.x > 1) cluster_barrier(); else __syncthreads();
   }
   if (rank != 0) return;
-  if (i < 0) {  // an empty request
-    for (int x = threadIdx.x; x < g.G * kD; x += kGateWarps * 32) O[row0 * kD + x] = __float2bfloat16(0.f);
-    for (int x = threadIdx.x; x < g.G; x += kGateWarps * 32) LSE[row0 + x] = -INFINITY;
-  }
   const int m = min(g.k - 1, max(i, 0)), HT = (g.G + 7) / 8;
   for (int ht = 0; ht < HT; ++ht) {
     const int hh = ht * 8 + warp, heads = min(8, g.G - ht * 8);
@@ -175,7 +170,6 @@ __global__ void __launch_bounds__(kGateWarps * 32)
         sel[(row0 + hh) * g.k + lane] = mine;
         s_sel[warp][lane] = mine;
       }
-      if (lane == 0) w.arrived[row0 + hh] = 0;
     }
     __syncthreads();
     if (warp == 0) {
@@ -308,7 +302,6 @@ struct Piece {
   int chunk;              // of the block
   int key0, n, left;      // first key in the block, keys here, keys of the unit behind this piece
   uint32_t slots[2];
-  int own_chunks, parts;  // chunks of the request's own block, and of all blocks of one head
   bool begins;            // first piece of its unit
 };
 
@@ -320,13 +313,12 @@ __device__ __forceinline__ void open_unit(const CacheGeom& g, const CacheDecodeW
   p.s = sg / g.Hkv;
   const int32_t len = cached_len(g, lens, p.s);
   const int own = (len - 1) / g.bs, own_n = len - own * g.bs;
-  p.own_chunks = (own_n + w.CK - 1) / w.CK;
-  p.parts = p.own_chunks + min(g.k - 1, own) * w.NC;
+  const int own_chunks = (own_n + w.CK - 1) / w.CK;
   int seg = 0, bn = own_n;
   p.chunk = p.unit;
-  if (p.unit >= p.own_chunks) {
-    seg = 1 + (p.unit - p.own_chunks) / w.NC;
-    p.chunk = (p.unit - p.own_chunks) % w.NC;
+  if (p.unit >= own_chunks) {
+    seg = 1 + (p.unit - own_chunks) / w.NC;
+    p.chunk = (p.unit - own_chunks) % w.NC;
     bn = g.bs;
   }
   const int4 e = __ldg(reinterpret_cast<const int4*>(w.segs + (size_t)p.idx * w.max_segs + seg));
@@ -340,77 +332,11 @@ __device__ __forceinline__ void open_unit(const CacheGeom& g, const CacheDecodeW
   p.begins = true;
 }
 
-// Adds 1; what the warp wrote before (and synchronised) is seen by whoever sees the new value.
-__device__ __forceinline__ int atomic_inc_acq_rel(int32_t* p) {
-  int old;
-  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(p) : "memory");
-  return old;
-}
-
-// The partial results of one (request, head), merged by online softmax (log2 units) by one warp.
-template <int kD>
-__device__ __forceinline__ void merge_row(const CacheGeom& g, const CacheDecodeWork& w, size_t row, int own_chunks, int n,
-                                          __nv_bfloat16* __restrict__ O, float* __restrict__ LSE) {
-  constexpr int kDL = kD / 32;
-  const int lane = threadIdx.x & 31;
-  const float2* ml = w.part_ml + row * g.k * w.NC;
-  const float* po = w.part_o + row * g.k * w.NC * kD + lane * kDL;
-  auto at = [&](int x) { return x < own_chunks ? x : w.NC + (x - own_chunks); };
-  float M = -INFINITY;
-  float2 held = make_float2(-INFINITY, 0.f);  // of part `lane`
-  if (lane < n) held = __ldcg(&ml[at(lane)]);
-  M = held.x;
-  for (int x = 32 + lane; x < n; x += 32) M = fmaxf(M, __ldcg(&ml[at(x)]).x);
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  const float base = M == -INFINITY ? 0.f : M;
-  float L = 0.f, acc[kDL];
-#pragma unroll
-  for (int d = 0; d < kDL; ++d) acc[d] = 0.f;
-  for (int x0 = 0; x0 < n; x0 += 32) {
-    if (x0 > 0) {
-      held = make_float2(-INFINITY, 0.f);
-      if (x0 + lane < n) held = __ldcg(&ml[at(x0 + lane)]);
-    }
-    const float wt = ex2(held.x - base);  // 0 behind the last part
-    L = fmaf(held.y, wt, L);
-    for (int x1 = x0; x1 < min(n, x0 + 32); x1 += 16) {  // 16 rows on their way at a time
-      float f[16][kDL];
-#pragma unroll
-      for (int x = 0; x < 16; ++x) {
-        const float* src = po + (size_t)at(min(x1 + x, n - 1)) * kD;
-        if constexpr (kDL == 4) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-          f[x][0] = v.x, f[x][1] = v.y, f[x][2] = v.z, f[x][3] = v.w;
-        } else {
-          const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-          f[x][0] = v.x, f[x][1] = v.y;
-        }
-      }
-#pragma unroll
-      for (int x = 0; x < 16; ++x) {
-        const float wx = __shfl_sync(0xffffffffu, wt, (x1 + x) & 31);
-        if (x1 + x < n)
-#pragma unroll
-          for (int d = 0; d < kDL; ++d) acc[d] = fmaf(wx, f[x][d], acc[d]);
-      }
-    }
-  }
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-  const float inv = L == 0.f ? 0.f : 1.f / L;  // 0: no key at all
-#pragma unroll
-  for (int d = 0; d < kDL; d += 2)
-    *reinterpret_cast<__nv_bfloat162*>(O + row * kD + lane * kDL + d) = __floats2bfloat162_rn(acc[d] * inv, acc[d + 1] * inv);
-  if (lane == 0) LSE[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2C;
-}
-
 template <int kD, int kFmt>
 __global__ void __launch_bounds__(kAttnWarps * 32, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, CacheGeom g,
                       const __nv_bfloat16* __restrict__ Q, const float* __restrict__ Ks, const float* __restrict__ Vs,
-                      const int32_t* __restrict__ lens, const int32_t* __restrict__ tables, CacheDecodeWork w, int NI,
-                      __nv_bfloat16* __restrict__ O, float* __restrict__ LSE) {
+                      const int32_t* __restrict__ lens, const int32_t* __restrict__ tables, CacheDecodeWork w, int NI) {
   using L = AttnLayout<kD>;
   constexpr int kW = kD / 16;   // k steps of K Q^T = 16-row tiles of V^T
   extern __shared__ uint8_t smem_raw[];
@@ -427,6 +353,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1)
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
   }
+  launch_dependents();
   wait_for_primary();  // the gate's results
 
   // ---- units before each group of `per` entries of the work list
@@ -722,14 +649,6 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1)
           if (gq == 0) w.part_ml[part] = make_float2(m[e], ls[e]);
         }
       }
-      // whoever brings a row's last part merges it (the gate has set the counters to 0)
-      __syncwarp();
-      const size_t row0 = (size_t)cur.s * g.Hq + (size_t)cur.gk * g.G + cur.ht * 8;
-      bool last = false;
-      if (lane < 8 && (((lane < 4 ? cur.slots[0] : cur.slots[1]) >> 8 * (lane & 3)) & 0xffu) != 0xffu)
-        last = atomic_inc_acq_rel(w.arrived + row0 + lane) == cur.parts - 1;
-      uint32_t rows = __ballot_sync(0xffffffffu, last);
-      for (; rows; rows &= rows - 1) merge_row<kD>(g, w, row0 + __ffs(rows) - 1, cur.own_chunks, cur.parts, O, LSE);
     }
     if (!more) break;
     cur = nxt;
@@ -747,6 +666,87 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1)
       mbar_wait_warp(&full[rd], parity, g.err);
       if (++rd == kStages) rd = 0, parity ^= 1;
     }
+}
+
+// Partial results of a (request, head), merged by online softmax (log2 units) by kWarps warps: warp x
+// takes every kWarps-th part.
+constexpr int kMergeWarps = 4;  // of a CTA
+
+template <int kD, int kWarps>
+__global__ void __launch_bounds__(kMergeWarps * 32)
+    cache_merge_kernel(CacheGeom g, const int32_t* __restrict__ lens, CacheDecodeWork w, __nv_bfloat16* __restrict__ O,
+                       float* __restrict__ LSE) {
+  constexpr int kDL = kD / 32;
+  __shared__ float s_acc[kMergeWarps][kD], s_l[kMergeWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % kWarps;
+  const size_t row = (size_t)blockIdx.x * (kMergeWarps / kWarps) + warp / kWarps;
+  const bool live = row < (size_t)g.B * g.Hq;
+  const int32_t len = live ? cached_len(g, lens, (int)(row / g.Hq)) : 0;
+  const int own = len > 0 ? (len - 1) / g.bs : 0, own_chunks = (len - own * g.bs + w.CK - 1) / w.CK;
+  const int n = own_chunks + min(g.k - 1, own) * w.NC;  // slots are filled from the front
+  const float2* ml = w.part_ml + row * g.k * w.NC;
+  const float* po = w.part_o + row * g.k * w.NC * kD + lane * kDL;
+  auto at = [&](int x) { return x < own_chunks ? x : w.NC + (x - own_chunks); };
+  wait_for_primary();
+  float M = -INFINITY;
+  for (int x = lane; x < n; x += 32) M = fmaxf(M, ml[at(x)].x);
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  const float base = M == -INFINITY ? 0.f : M;
+  float L = 0.f, acc[kDL];
+#pragma unroll
+  for (int d = 0; d < kDL; ++d) acc[d] = 0.f;
+  const int mine = n > part ? (n - part + kWarps - 1) / kWarps : 0;  // parts of this warp
+  for (int x0 = 0; x0 < mine; x0 += 32) {
+    float wt = 0.f;
+    if (x0 + lane < mine) {
+      const float2 v = ml[at(part + (x0 + lane) * kWarps)];
+      wt = ex2(v.x - base);
+      L = fmaf(v.y, wt, L);
+    }
+    for (int x1 = x0; x1 < min(mine, x0 + 32); x1 += 8) {  // 8 rows on their way at a time
+      float f[8][kDL];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const float* src = po + (size_t)at(part + min(x1 + x, mine - 1) * kWarps) * kD;
+        if constexpr (kDL == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          f[x][0] = v.x, f[x][1] = v.y, f[x][2] = v.z, f[x][3] = v.w;
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(src);
+          f[x][0] = v.x, f[x][1] = v.y;
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const float wx = __shfl_sync(0xffffffffu, wt, (x1 + x) & 31);
+        if (x1 + x < mine)
+#pragma unroll
+          for (int d = 0; d < kDL; ++d) acc[d] = fmaf(wx, f[x][d], acc[d]);
+      }
+    }
+  }
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+  if constexpr (kWarps > 1) {
+    if (lane == 0) s_l[warp] = L;
+#pragma unroll
+    for (int d = 0; d < kDL; ++d) s_acc[warp][lane * kDL + d] = acc[d];
+    __syncthreads();
+    if (part > 0) return;
+#pragma unroll
+    for (int x = 1; x < kWarps; ++x) {
+      L += s_l[warp + x];
+#pragma unroll
+      for (int d = 0; d < kDL; ++d) acc[d] += s_acc[warp + x][lane * kDL + d];
+    }
+  }
+  if (!live) return;
+  const float inv = L == 0.f ? 0.f : 1.f / L;  // 0: no key at all
+#pragma unroll
+  for (int d = 0; d < kDL; d += 2)
+    *reinterpret_cast<__nv_bfloat162*>(O + row * kD + lane * kDL + d) = __floats2bfloat162_rn(acc[d] * inv, acc[d + 1] * inv);
+  if (lane == 0) LSE[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2C;
 }
 
 // ---------------------------------------------------------------------------------- launch
@@ -776,7 +776,7 @@ cudaError_t make_codes_map(CUtensorMap* m, const void* base, const CacheGeom& g)
 
 template <int kD, int kH>
 cudaError_t launch_gate(const CacheGeom& g, const __nv_bfloat16* Q, const float* Kbar, const int32_t* lens,
-                        int32_t* sel, const CacheDecodeWork& w, __nv_bfloat16* O, float* LSE, cudaStream_t st) {
+                        int32_t* sel, const CacheDecodeWork& w, cudaStream_t st) {
   // CTAs of a cluster share the candidates, 64 blocks each at a time
   int c = 1;
   while (c < 8 && g.k > 1 && c * kGateWarps * kGateRows < g.MB - 1) c *= 2;
@@ -790,7 +790,23 @@ cudaError_t launch_gate(const CacheGeom& g, const __nv_bfloat16* Q, const float*
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_gate_kernel<kD, kH>, g, Q, Kbar, lens, sel, w, O, LSE);
+  return cudaLaunchKernelEx(&cfg, cache_gate_kernel<kD, kH>, g, Q, Kbar, lens, sel, w);
+}
+
+// A kernel whose CTAs may start while the one before it runs, and wait for its results there.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(dim3 grid, int threads, size_t smem, cudaStream_t st, void (*kernel)(P...), A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
 template <int kD, int kFmt>
@@ -798,9 +814,9 @@ cudaError_t launch_decode_t(const CacheGeom& g, const __nv_bfloat16* Q, const ui
                             const float* Ks, const float* Vs, const float* Kbar, const int32_t* lens,
                             const int32_t* tables, int32_t* sel, const CacheDecodeWork& w, __nv_bfloat16* O,
                             float* LSE, int sms, cudaStream_t st) {
-  cudaError_t e = g.G == 1   ? launch_gate<kD, 1>(g, Q, Kbar, lens, sel, w, O, LSE, st)
-                  : g.G == 2 ? launch_gate<kD, 2>(g, Q, Kbar, lens, sel, w, O, LSE, st)
-                             : launch_gate<kD, 4>(g, Q, Kbar, lens, sel, w, O, LSE, st);
+  cudaError_t e = g.G == 1   ? launch_gate<kD, 1>(g, Q, Kbar, lens, sel, w, st)
+                  : g.G == 2 ? launch_gate<kD, 2>(g, Q, Kbar, lens, sel, w, st)
+                             : launch_gate<kD, 4>(g, Q, Kbar, lens, sel, w, st);
   if (e != cudaSuccess) return e;
   CUtensorMap tk, tv;
   if ((e = make_codes_map(&tk, Kc, g)) != cudaSuccess) return e;
@@ -808,17 +824,16 @@ cudaError_t launch_decode_t(const CacheGeom& g, const __nv_bfloat16* Q, const ui
   auto attn = cache_attn_kernel<kD, kFmt>;
   if ((e = cudaFuncSetAttribute(attn, cudaFuncAttributeMaxDynamicSharedMemorySize, AttnLayout<kD>::kAlloc)) != cudaSuccess)
     return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)sms);
-  cfg.blockDim = dim3(kAttnWarps * 32);
-  cfg.dynamicSmemBytes = AttnLayout<kD>::kAlloc;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];  // its CTAs may start while the gate runs, and wait for its results there
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn, tk, tv, g, Q, Ks, Vs, lens, tables, w, g.B * g.Hkv * ((g.G + 7) / 8), O, LSE);
+  e = launch_dependent(dim3((unsigned)sms), kAttnWarps * 32, AttnLayout<kD>::kAlloc, st, attn, tk, tv, g, Q, Ks, Vs,
+                       lens, tables, w, g.B * g.Hkv * ((g.G + 7) / 8));
+  if (e != cudaSuccess) return e;
+  // many parts: all warps of a CTA on one row
+  const int64_t rows = (int64_t)g.B * g.Hq;
+  if (g.k * w.NC > 8)
+    return launch_dependent(dim3((unsigned)rows), kMergeWarps * 32, 0, st, cache_merge_kernel<kD, kMergeWarps>, g, lens, w,
+                            O, LSE);
+  return launch_dependent(dim3((unsigned)((rows + kMergeWarps - 1) / kMergeWarps)), kMergeWarps * 32, 0, st,
+                          cache_merge_kernel<kD, 1>, g, lens, w, O, LSE);
 }
 
 }  // namespace
