@@ -72,7 +72,7 @@ __device__ __forceinline__ uint32_t float2_to_codes2(float a, float b) {
 // A block that heads of one tile of 8 chose: byte h of slots is head h's slot, 0xff if it did not.
 struct __align__(16) CacheSeg {
   int32_t block;
-  int32_t pad;
+  int32_t keys;        // of the block: bs, or those up to the newest token
   uint32_t slots[2];
 };
 
@@ -80,7 +80,7 @@ struct __align__(16) CacheSeg {
 // list is a (request, KV head, tile of 8 heads), its units are chunks of CK keys.
 struct CacheDecodeWork {
   uint64_t* score;   // [B, Hq, MB] gate scores, as ordered keys
-  CacheSeg* segs;    // [entries, max_segs] distinct blocks, the own one first
+  CacheSeg* segs;    // [entries, max_segs] distinct blocks, the own one last
   int32_t* units;    // [entries] chunks in all
   float* part_o;     // [B, Hq, k, NC, D] partial sums of weighted values
   float2* part_ml;   // [B, Hq, k, NC] running maximum (log2 units), sum of the softmax

@@ -175,19 +175,13 @@ __global__ void __launch_bounds__(kGateWarps * 32)
     if (warp == 0) {
       const size_t idx = ((size_t)s * g.Hkv + gk) * HT + ht;
       CacheSeg* segs = w.segs + idx * w.max_segs;
-      // the own block is every head's slot 0; heads beyond the group take nothing
-      if (lane == 0 && i >= 0) {
-        CacheSeg own{i, 0, {~0u, ~0u}};
-        for (int h = 0; h < heads; ++h) own.slots[h >> 2] &= ~(0xffu << 8 * (h & 3));
-        segs[0] = own;
-      }
-      int count = i >= 0 ? 1 : 0;
+      int count = 0;
       const int n = heads * m;  // chosen (head, slot) pairs, head by head
       for (int e0 = 0; e0 < n; e0 += 32) {
         const int e = e0 + lane, eh = e / m, ej = 1 + e - eh * m;
         const int32_t b = e < n ? s_sel[eh][ej] : -1;
         bool first = e < n;
-        CacheSeg seg{b, 0, {~0u, ~0u}};
+        CacheSeg seg{b, g.bs, {~0u, ~0u}};
         for (int oh = 0; oh < heads; ++oh)
           for (int oj = 1; oj <= m; ++oj)
             if (e < n && s_sel[oh][oj] == b) {
@@ -199,9 +193,11 @@ __global__ void __launch_bounds__(kGateWarps * 32)
         if (first) segs[count + __popc(firsts & ((1u << lane) - 1))] = seg;
         count += __popc(firsts);
       }
-      if (lane == 0) {
-        const int own_n = len - max(i, 0) * g.bs;  // 0 where the request is empty
-        w.units[idx] = count ? (own_n + w.CK - 1) / w.CK + (count - 1) * w.NC : 0;
+      if (lane == 0) {  // last the own block, every head's slot 0; heads beyond the group take nothing
+        CacheSeg own{i, len - max(i, 0) * g.bs, {~0u, ~0u}};
+        for (int h = 0; h < heads; ++h) own.slots[h >> 2] &= ~(0xffu << 8 * (h & 3));
+        if (i >= 0) segs[count] = own;
+        w.units[idx] = count * w.NC + (own.keys + w.CK - 1) / w.CK;  // 0 where the request is empty
       }
     }
     __syncthreads();
@@ -241,6 +237,7 @@ struct AttnLayout {
   static constexpr int kMaxPrefix = 2048;                   // units are scanned in so many groups
   static constexpr int kBytes = kPrefix + (kMaxPrefix + 1) * 4 + kAttnWarps * 4;
   static constexpr int kAlloc = kBytes + 1024;
+  static constexpr int kCtas = 1;            // on an SM
 };
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) { return __byte_perm(a, b, s); }
@@ -296,7 +293,7 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 
 // A run of at most kPiece keys of one unit (uniform over the warp).
 struct Piece {
-  int idx, unit;          // place in the work list
+  int idx;                // entry of the work list
   int s, gk, ht;
   int32_t block;
   int chunk;              // of the block
@@ -305,35 +302,8 @@ struct Piece {
   bool begins;            // first piece of its unit
 };
 
-__device__ __forceinline__ void open_unit(const CacheGeom& g, const CacheDecodeWork& w, const int32_t* lens, Piece& p) {
-  const int HT = (g.G + 7) / 8;
-  p.ht = p.idx % HT;
-  const int sg = p.idx / HT;
-  p.gk = sg % g.Hkv;
-  p.s = sg / g.Hkv;
-  const int32_t len = cached_len(g, lens, p.s);
-  const int own = (len - 1) / g.bs, own_n = len - own * g.bs;
-  const int own_chunks = (own_n + w.CK - 1) / w.CK;
-  int seg = 0, bn = own_n;
-  p.chunk = p.unit;
-  if (p.unit >= own_chunks) {
-    seg = 1 + (p.unit - own_chunks) / w.NC;
-    p.chunk = (p.unit - own_chunks) % w.NC;
-    bn = g.bs;
-  }
-  const int4 e = __ldg(reinterpret_cast<const int4*>(w.segs + (size_t)p.idx * w.max_segs + seg));
-  p.block = e.x;
-  p.slots[0] = (uint32_t)e.z;
-  p.slots[1] = (uint32_t)e.w;
-  p.key0 = p.chunk * w.CK;
-  const int n = min(w.CK, bn - p.key0);
-  p.n = min(n, kPiece);
-  p.left = n - p.n;
-  p.begins = true;
-}
-
 template <int kD, int kFmt>
-__global__ void __launch_bounds__(kAttnWarps * 32, 1)
+__global__ void __launch_bounds__(kAttnWarps * 32, AttnLayout<kD>::kCtas)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, CacheGeom g,
                       const __nv_bfloat16* __restrict__ Q, const float* __restrict__ Ks, const float* __restrict__ Vs,
                       const int32_t* __restrict__ lens, const int32_t* __restrict__ tables, CacheDecodeWork w, int NI) {
@@ -365,7 +335,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1)
     const int gr = threadIdx.x * kEach + x;
     cnt[x] = 0;
     if (gr < groups)
-      for (int y = gr * per; y < min(NI, (gr + 1) * per); ++y) cnt[x] += w.units[y];
+      for (int y = gr * per; y < min(NI, (gr + 1) * per); ++y) cnt[x] += __ldcg(w.units + y);
     sum += cnt[x];
   }
   int32_t inc = sum;
@@ -390,8 +360,14 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1)
   int32_t todo = (int32_t)((wid + 1) * total / W) - (int32_t)(wid * total / W);  // units of this warp
   if (todo == 0) return;
 
-  // ---- the first unit
-  Piece cur, nxt;
+  // ---- work ahead: the description of the unit after the next piece is on its way while that piece's
+  // pages are, so that none of these loads is waited for
+  int n_idx, n_unit;  // the next unit to be opened
+  int4 n_seg = make_int4(0, 0, 0, 0);
+  auto units_of = [&](int idx) { return per == 1 ? prefix[idx + 1] - prefix[idx] : __ldcg(w.units + idx); };
+  auto fetch_seg = [&]() {
+    n_seg = __ldcg(reinterpret_cast<const int4*>(w.segs + (size_t)n_idx * w.max_segs + n_unit / w.NC));
+  };
   {
     const int32_t u = (int32_t)(wid * total / W);
     int lo = 0, hi = groups - 1;
@@ -399,38 +375,61 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1)
       const int mid = (lo + hi + 1) >> 1;
       if (prefix[mid] <= u) lo = mid; else hi = mid - 1;
     }
-    cur.idx = lo * per;
-    cur.unit = u - prefix[lo];
-    for (int32_t c; cur.unit >= (c = w.units[cur.idx]);) cur.unit -= c, ++cur.idx;
-    open_unit(g, w, lens, cur);
+    n_idx = lo * per;
+    n_unit = u - prefix[lo];
+    for (int32_t c; n_unit >= (c = units_of(n_idx));) n_unit -= c, ++n_idx;
+    fetch_seg();
   }
-  // The piece after p; false behind the warp's last one.
+  // The piece after p into o (p: the last one, or idx -1); false behind the warp's last one.
   auto advance = [&](const Piece& p, Piece& o) -> bool {
-    o = p;
     if (p.left > 0) {
+      o = p;
       o.key0 = p.key0 + p.n;
       o.n = min(p.left, kPiece);
       o.left = p.left - o.n;
       o.begins = false;
       return true;
     }
-    if (--todo == 0) return false;
-    ++o.unit;
-    while (o.unit >= w.units[o.idx]) o.unit = 0, ++o.idx;
-    open_unit(g, w, lens, o);
+    if (todo == 0) return false;
+    o.idx = n_idx;
+    o.s = p.s, o.gk = p.gk, o.ht = p.ht;
+    if (n_idx != p.idx) {
+      const int HT = (g.G + 7) / 8, sg = n_idx / HT;
+      o.ht = n_idx - sg * HT;
+      o.s = sg / g.Hkv;
+      o.gk = sg - o.s * g.Hkv;
+    }
+    o.chunk = n_unit % w.NC;
+    o.block = n_seg.x;
+    o.slots[0] = (uint32_t)n_seg.z;
+    o.slots[1] = (uint32_t)n_seg.w;
+    o.key0 = o.chunk * w.CK;
+    const int n = min(w.CK, n_seg.y - o.key0);
+    o.n = min(n, kPiece);
+    o.left = n - o.n;
+    o.begins = true;
+    ++n_unit;
+    if (--todo > 0) {
+      while (n_unit >= units_of(n_idx)) n_unit = 0, ++n_idx;
+      fetch_seg();
+    }
     return true;
   };
-  // Page of the lane-th run of ps keys (-1: none; bad ones are reported) and the pages' scales.
+  const int lps = 31 - __clz(g.ps);
+  // Page of the lane-th run of ps keys (-1: none), not yet looked at.
   auto pages_of = [&](const Piece& p) -> int32_t {
-    int32_t page = -1;
-    if (lane * g.ps < p.n) {
-      page = __ldg(tables + (size_t)p.s * g.MP + (p.block * g.bs + p.key0) / g.ps + lane);
-      if (!page_ok(g, page)) {
-        atomicOr(g.err, kErrBadPage);
-        page = -1;
-      }
+    return lane << lps < p.n ? __ldg(tables + (size_t)p.s * g.MP + ((p.block * g.bs + p.key0) >> lps) + lane) : -1;
+  };
+  // Bad pages become -1 and are reported; the others' scales are fetched.
+  auto look_at = [&](const Piece& p, int32_t& page, float& ks, float& vs) {
+    ks = 0.f, vs = 1.f;
+    if (page_ok(g, page)) {
+      ks = __ldg(Ks + (size_t)page * g.Hkv + p.gk);
+      vs = __ldg(Vs + (size_t)page * g.Hkv + p.gk);
+    } else {
+      if (lane << lps < p.n) atomicOr(g.err, kErrBadPage);
+      page = -1;
     }
-    return page;
   };
   const int box = min(g.ps, kTile);
   int wr = 0;  // stage that the next copy goes to
@@ -440,7 +439,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1)
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int key = tile * kTile + x * box;
-      pg[x] = __shfl_sync(0xffffffffu, page, (key / g.ps) & 31);
+      pg[x] = __shfl_sync(0xffffffffu, page, key >> lps & 31);
       if (x * box >= kTile || key >= p.n) pg[x] = -1;
     }
     if (lane == 0) {
@@ -449,7 +448,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1)
 #pragma unroll
       for (int x = 0; x < 2; ++x)
         if (pg[x] >= 0) {
-          const int row = (p.key0 + tile * kTile + x * box) % g.ps, slab = pg[x] * g.Hkv + p.gk;
+          const int row = (p.key0 + tile * kTile + x * box) & (g.ps - 1), slab = pg[x] * g.Hkv + p.gk;
           tma_load_3d(dst + x * box * kD, &tmK, &full[wr], 0, row, slab);
           tma_load_3d(dst + L::kHalf + x * box * kD, &tmV, &full[wr], 0, row, slab);
         }
@@ -458,13 +457,17 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1)
   };
   auto tiles_of = [](const Piece& p) { return (p.n + kTile - 1) / kTile; };
 
+  Piece cur, nxt;
+  nxt.idx = -1;
+  nxt.left = 0;
+  advance(nxt, cur);
   int32_t page_c = pages_of(cur), page_n = -1;
+  float ks, vs, ks_n = 0.f, vs_n = 1.f;
+  look_at(cur, page_c, ks, vs);
   int issued_c = 0, issued_n = 0, flying = 0;
   for (; issued_c < min(tiles_of(cur), kStages); ++issued_c, ++flying) issue(cur, page_c, issued_c);
-  bool more = advance(cur, nxt), ok = true;
+  bool more = advance(cur, nxt), looked = false, ok = true;
   if (more) page_n = pages_of(nxt);
-  float ks = page_c >= 0 ? __ldg(Ks + (size_t)page_c * g.Hkv + cur.gk) : 0.f;
-  float vs = page_c >= 0 ? __ldg(Vs + (size_t)page_c * g.Hkv + cur.gk) : 1.f;
   int rd = 0;
   uint32_t parity = 0;
 
@@ -554,7 +557,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1)
       float mx0 = m[0], mx1 = m[1];
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
-        const int key = tile * kTile + mt * 16, pi = (key / g.ps) & 31;
+        const int key = tile * kTile + mt * 16, pi = key >> lps & 31;
         const float k1 = __shfl_sync(0xffffffffu, ks, pi), lv = __shfl_sync(0xffffffffu, lvs, pi);
         const int32_t pg = __shfl_sync(0xffffffffu, page_c, pi);
         live[mt] = pg >= 0 ? min(16, cur.n - key) : 0;
@@ -625,7 +628,10 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1)
       if (++rd == kStages) rd = 0, parity ^= 1;
       --flying;
       if (issued_c < tiles) issue(cur, page_c, issued_c++), ++flying;
-      else if (more && issued_n < tiles_of(nxt)) issue(nxt, page_n, issued_n++), ++flying;
+      else if (more) {
+        if (!looked) look_at(nxt, page_n, ks_n, vs_n), looked = true;
+        if (issued_n < tiles_of(nxt)) issue(nxt, page_n, issued_n++), ++flying;
+      }
     }
     if (!ok) break;
     if (cur.left == 0) {
@@ -651,15 +657,17 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1)
       }
     }
     if (!more) break;
+    if (!looked) look_at(nxt, page_n, ks_n, vs_n);
     cur = nxt;
     page_c = page_n;
+    ks = ks_n;
+    vs = vs_n;
     issued_c = issued_n;
     issued_n = 0;
-    ks = page_c >= 0 ? __ldg(Ks + (size_t)page_c * g.Hkv + cur.gk) : 0.f;
-    vs = page_c >= 0 ? __ldg(Vs + (size_t)page_c * g.Hkv + cur.gk) : 1.f;
     for (; flying < kStages && issued_c < tiles_of(cur); ++flying) issue(cur, page_c, issued_c++);
     more = advance(cur, nxt);
-    page_n = more ? pages_of(nxt) : -1;
+    looked = false;
+    if (more) page_n = pages_of(nxt);
   }
   if (!ok)  // a wait gave up: leave no copy behind
     for (; flying > 0; --flying) {
@@ -689,7 +697,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   auto at = [&](int x) { return x < own_chunks ? x : w.NC + (x - own_chunks); };
   wait_for_primary();
   float M = -INFINITY;
-  for (int x = lane; x < n; x += 32) M = fmaxf(M, ml[at(x)].x);
+  for (int x = lane; x < n; x += 32) M = fmaxf(M, __ldcg(ml + at(x)).x);
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
   const float base = M == -INFINITY ? 0.f : M;
@@ -700,7 +708,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   for (int x0 = 0; x0 < mine; x0 += 32) {
     float wt = 0.f;
     if (x0 + lane < mine) {
-      const float2 v = ml[at(part + (x0 + lane) * kWarps)];
+      const float2 v = __ldcg(ml + at(part + (x0 + lane) * kWarps));
       wt = ex2(v.x - base);
       L = fmaf(v.y, wt, L);
     }
@@ -710,10 +718,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
       for (int x = 0; x < 8; ++x) {
         const float* src = po + (size_t)at(part + min(x1 + x, mine - 1) * kWarps) * kD;
         if constexpr (kDL == 4) {
-          const float4 v = *reinterpret_cast<const float4*>(src);
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
           f[x][0] = v.x, f[x][1] = v.y, f[x][2] = v.z, f[x][3] = v.w;
         } else {
-          const float2 v = *reinterpret_cast<const float2*>(src);
+          const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
           f[x][0] = v.x, f[x][1] = v.y;
         }
       }
@@ -824,7 +832,7 @@ cudaError_t launch_decode_t(const CacheGeom& g, const __nv_bfloat16* Q, const ui
   auto attn = cache_attn_kernel<kD, kFmt>;
   if ((e = cudaFuncSetAttribute(attn, cudaFuncAttributeMaxDynamicSharedMemorySize, AttnLayout<kD>::kAlloc)) != cudaSuccess)
     return e;
-  e = launch_dependent(dim3((unsigned)sms), kAttnWarps * 32, AttnLayout<kD>::kAlloc, st, attn, tk, tv, g, Q, Ks, Vs,
+  e = launch_dependent(dim3((unsigned)(sms * AttnLayout<kD>::kCtas)), kAttnWarps * 32, AttnLayout<kD>::kAlloc, st, attn, tk, tv, g, Q, Ks, Vs,
                        lens, tables, w, g.B * g.Hkv * ((g.G + 7) / 8));
   if (e != cudaSuccess) return e;
   // many parts: all warps of a CTA on one row
@@ -838,19 +846,15 @@ cudaError_t launch_decode_t(const CacheGeom& g, const __nv_bfloat16* Q, const ui
 
 }  // namespace
 
-// Keys of a unit, a power of two so that the pieces of every unit start on a page.  Long chunks write
-// and merge fewer partial rows, short ones spread a small problem over the GPU.  Counting the units
-// that there are at the least (all heads of a group agree): the longest chunks that still give every
-// warp two units; a problem too small for that with chunks of 512 takes at most 512, and as many fewer
-// as give every second warp a unit (half of the warps have copies enough in flight to fill the memory).
+// Keys of a unit, a power of two so that the pieces of every unit start on a page: the longest that
+// leaves every warp four units if all heads of a group agree (more where they do not), at least 128.
+// Longer ones write and merge fewer partial rows, shorter ones leave less to the slowest warp.
 int cache_chunk_keys(const CacheGeom& g) {
-  const int64_t rows = (int64_t)g.B * g.Hkv * ((g.G + 7) / 8) * g.k, warps = 148 * kAttnWarps;
-  auto longest = [&](int64_t units, int ck) {
-    while (ck > 128 && (ck / 2 >= g.bs || rows * ((g.bs + ck - 1) / ck) < units)) ck /= 2;
-    return ck;
-  };
-  const int most = longest(2 * warps, 8192);
-  return most >= 512 ? most : longest(warps / 2, 512);
+  const int64_t rows = (int64_t)g.B * g.Hkv * ((g.G + 7) / 8) * g.k;
+  const int64_t warps = 148 * kAttnWarps * (g.D == 64 ? AttnLayout<64>::kCtas : AttnLayout<128>::kCtas);
+  int ck = 8192;
+  while (ck > 128 && (ck / 2 >= g.bs || rows * ((g.bs + ck - 1) / ck) < 4 * warps)) ck /= 2;
+  return ck;
 }
 
 cudaError_t launch_cache_decode(const CacheGeom& g, const __nv_bfloat16* Q, const uint8_t* Kc, const uint8_t* Vc,
