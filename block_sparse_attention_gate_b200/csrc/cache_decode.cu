@@ -225,19 +225,18 @@ __global__ void __launch_bounds__(kGateWarps * 32)
 
 constexpr int kTile = 32;       // keys of a stage
 constexpr int kPiece = 256;     // keys whose pages a warp holds at a time (at most 16 pages)
-constexpr int kAttnWarps = 8;
-constexpr int kStages = 3;
 
 template <int kD>
 struct AttnLayout {
+  static constexpr int kWarps = kD == 64 ? 12 : 8;
+  static constexpr int kStages = kD == 64 ? 4 : 3;
   static constexpr int kHalf = kTile * kD;                  // codes of K (or V) of a stage
-  static constexpr int kWarp = kStages * 2 * kHalf;
-  static constexpr int kBar = kAttnWarps * kWarp;           // after the rings
-  static constexpr int kPrefix = kBar + kAttnWarps * kStages * 8;
-  static constexpr int kMaxPrefix = 2048;                   // units are scanned in so many groups
-  static constexpr int kBytes = kPrefix + (kMaxPrefix + 1) * 4 + kAttnWarps * 4;
+  static constexpr int kRing = kStages * 2 * kHalf;         // of a warp
+  static constexpr int kBar = kWarps * kRing;              // after the rings
+  static constexpr int kPrefix = kBar + kWarps * kStages * 8;
+  static constexpr int kMaxPrefix = kWarps * 32 * 6;    // units are scanned in so many groups
+  static constexpr int kBytes = kPrefix + (kMaxPrefix + 1) * 4 + kWarps * 4;
   static constexpr int kAlloc = kBytes + 1024;
-  static constexpr int kCtas = 1;            // on an SM
 };
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) { return __byte_perm(a, b, s); }
@@ -303,16 +302,17 @@ struct Piece {
 };
 
 template <int kD, int kFmt>
-__global__ void __launch_bounds__(kAttnWarps * 32, AttnLayout<kD>::kCtas)
+__global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, CacheGeom g,
                       const __nv_bfloat16* __restrict__ Q, const float* __restrict__ Ks, const float* __restrict__ Vs,
                       const int32_t* __restrict__ lens, const int32_t* __restrict__ tables, CacheDecodeWork w, int NI) {
   using L = AttnLayout<kD>;
+  constexpr int kStages = L::kStages;
   constexpr int kW = kD / 16;   // k steps of K Q^T = 16-row tiles of V^T
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, t = lane & 3;
-  uint8_t* ring = smem + warp * L::kWarp;
+  uint8_t* ring = smem + warp * L::kRing;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar) + warp * kStages;
   int32_t* prefix = reinterpret_cast<int32_t*>(smem + L::kPrefix);
   int32_t* wsum = prefix + L::kMaxPrefix + 1;
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, AttnLayout<kD>::kCtas)
 
   // ---- units before each group of `per` entries of the work list
   const int per = (NI + L::kMaxPrefix - 1) / L::kMaxPrefix, groups = (NI + per - 1) / per;
-  constexpr int kEach = L::kMaxPrefix / (kAttnWarps * 32);
+  constexpr int kEach = L::kMaxPrefix / (L::kWarps * 32);
   int32_t cnt[kEach], sum = 0;
 #pragma unroll
   for (int x = 0; x < kEach; ++x) {
@@ -353,10 +353,10 @@ __global__ void __launch_bounds__(kAttnWarps * 32, AttnLayout<kD>::kCtas)
     prefix[threadIdx.x * kEach + x] = before;
     before += cnt[x];
   }
-  if (threadIdx.x == kAttnWarps * 32 - 1) prefix[L::kMaxPrefix] = before;
+  if (threadIdx.x == L::kWarps * 32 - 1) prefix[L::kMaxPrefix] = before;
   __syncthreads();
   const int32_t total = prefix[L::kMaxPrefix];
-  const int64_t W = (int64_t)gridDim.x * kAttnWarps, wid = (int64_t)blockIdx.x * kAttnWarps + warp;
+  const int64_t W = (int64_t)gridDim.x * L::kWarps, wid = (int64_t)blockIdx.x * L::kWarps + warp;
   int32_t todo = (int32_t)((wid + 1) * total / W) - (int32_t)(wid * total / W);  // units of this warp
   if (todo == 0) return;
 
@@ -832,7 +832,7 @@ cudaError_t launch_decode_t(const CacheGeom& g, const __nv_bfloat16* Q, const ui
   auto attn = cache_attn_kernel<kD, kFmt>;
   if ((e = cudaFuncSetAttribute(attn, cudaFuncAttributeMaxDynamicSharedMemorySize, AttnLayout<kD>::kAlloc)) != cudaSuccess)
     return e;
-  e = launch_dependent(dim3((unsigned)(sms * AttnLayout<kD>::kCtas)), kAttnWarps * 32, AttnLayout<kD>::kAlloc, st, attn, tk, tv, g, Q, Ks, Vs,
+  e = launch_dependent(dim3((unsigned)sms), AttnLayout<kD>::kWarps * 32, AttnLayout<kD>::kAlloc, st, attn, tk, tv, g, Q, Ks, Vs,
                        lens, tables, w, g.B * g.Hkv * ((g.G + 7) / 8));
   if (e != cudaSuccess) return e;
   // many parts: all warps of a CTA on one row
@@ -851,7 +851,7 @@ cudaError_t launch_decode_t(const CacheGeom& g, const __nv_bfloat16* Q, const ui
 // Longer ones write and merge fewer partial rows, shorter ones leave less to the slowest warp.
 int cache_chunk_keys(const CacheGeom& g) {
   const int64_t rows = (int64_t)g.B * g.Hkv * ((g.G + 7) / 8) * g.k;
-  const int64_t warps = 148 * kAttnWarps * (g.D == 64 ? AttnLayout<64>::kCtas : AttnLayout<128>::kCtas);
+  const int64_t warps = 148 * (g.D == 64 ? AttnLayout<64>::kWarps : AttnLayout<128>::kWarps);
   int ck = 8192;
   while (ck > 128 && (ck / 2 >= g.bs || rows * ((g.bs + ck - 1) / ck) < 4 * warps)) ck /= 2;
   return ck;
