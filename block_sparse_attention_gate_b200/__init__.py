@@ -320,15 +320,16 @@ class MobaCacheParams:
             raise MobaError(2, "format must be one of %s (got %r)" % (", ".join(CACHE_FORMATS), format))
         self.c = _CCacheParams(max_seqs, max_seqlen, num_pages, page_size, num_q_heads, num_kv_heads, head_dim,
                                block_size, top_k, CACHE_FORMATS[format], softmax_scale)
+        self._ref = ctypes.byref(self.c)
         self.format = format
         self.workspace_bytes = int(load().moba_cache_decode_workspace_size(self.ref()))
         if not self.workspace_bytes:
             raise MobaError(2, load().moba_last_error().decode())
-        c = self.c
         self.pages_per_seq = -(-max_seqlen // page_size)
         self.max_blocks = -(-max_seqlen // block_size)
-        i32, f32 = "torch.int32", "torch.float32"
-        code = "torch.float8_e4m3fn" if format == "e4m3" else "torch.int8"
+        import torch
+        i32, f32, bf16 = torch.int32, torch.float32, torch.bfloat16
+        code = torch.float8_e4m3fn if format == "e4m3" else torch.int8
         pool = (num_pages, num_kv_heads)
         # dtype and shape of every buffer (None: any length)
         self.buffers = {
@@ -336,25 +337,32 @@ class MobaCacheParams:
             "tables": (i32, (max_seqs, self.pages_per_seq)), "free_pages": (i32, (num_pages,)),
             "free_state": (i32, (2,)), "free_state_out": (i32, (2,)), "cu_new": (i32, (max_seqs + 1,)),
             "slots": (i32, (None,)), "status": (i32, (1,)),
-            "K": ("torch.bfloat16", (None, num_kv_heads, head_dim)),
-            "V": ("torch.bfloat16", (None, num_kv_heads, head_dim)),
+            "K": (bf16, (None, num_kv_heads, head_dim)), "V": (bf16, (None, num_kv_heads, head_dim)),
             "Kc": (code, pool + (page_size, head_dim)), "Vc": (code, pool + (page_size, head_dim)),
             "Ks": (f32, pool), "Vs": (f32, pool),
             "Kbar": (f32, (max_seqs, self.max_blocks, num_kv_heads, head_dim)),
-            "Q": ("torch.bfloat16", (max_seqs, num_q_heads, head_dim)),
-            "O": ("torch.bfloat16", (max_seqs, num_q_heads, head_dim)),
+            "Q": (bf16, (max_seqs, num_q_heads, head_dim)), "O": (bf16, (max_seqs, num_q_heads, head_dim)),
             "LSE": (f32, (max_seqs, num_q_heads)), "sel": (i32, (max_seqs, num_q_heads, top_k)),
         }
 
+        def specs(*names):
+            return tuple((n,) + self.buffers[n] for n in names)
+
+        self._tables = specs("add", "lens", "tables", "free_pages", "free_state", "lens_out", "free_state_out", "cu_new",
+                             "status")
+        self._append = specs("cu_new", "lens", "tables", "Kc", "Vc", "Ks", "Vs", "Kbar")
+        self._decode = specs("Q", "Kc", "Vc", "Ks", "Vs", "Kbar", "lens", "tables", "O", "LSE")
+        self._sel = specs("sel")
+
     def ref(self):
-        return ctypes.byref(self.c)
+        return self._ref
 
     def check(self, device, **tensors):
         """Every tensor has its dtype and shape, lies on `device` and is contiguous (K and V: in
         their last two dimensions)."""
         for name, t in tensors.items():
             dtype, shape = self.buffers[name]
-            if str(t.dtype) != dtype:
+            if t.dtype != dtype:
                 raise MobaError(1, "%s must be %s (got %s)" % (name, dtype, t.dtype))
             if len(t.shape) != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
                 raise MobaError(1, "%s must have shape %s (got %s)" % (
@@ -367,42 +375,82 @@ class MobaCacheParams:
             elif not t.is_contiguous():
                 raise MobaError(1, "%s must be contiguous" % name)
 
+    def _pointers(self, index, specs, tensors):
+        """Addresses of tensors that pass check(); the checks of a call are most of its time on the
+        host, so this form of them makes no strings and no device objects."""
+        out = []
+        for (name, dtype, shape), t in zip(specs, tensors):
+            if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+                self._check_one(name, t, index)
+            out.append(t.data_ptr())
+        return out
 
-def _on(device, stream, call):
-    """Calls with `device` current, on the given stream or that device's current one."""
+    def _check_one(self, name, t, index):
+        import torch
+        self.check(torch.device("cuda", index), **{name: t})
+
+    def _slots(self, index, slots):
+        if slots.dim() != 1 or slots.dtype is not self.buffers["slots"][0] or slots.get_device() != index or not slots.is_contiguous():
+            self._check_one("slots", slots, index)
+        return slots.data_ptr()
+
+
+def _on(t):
+    """The CUDA device index of a call's first tensor."""
+    index = t.get_device()
+    if index < 0:
+        raise MobaError(1, "the tensors must be on a CUDA device (got %s)" % t.device)
+    return index
+
+
+def _call(index, stream, fn, *args):
+    """fn(*args, stream) with device `index` current, on the given stream or its current one."""
     import torch
-    if device.type != "cuda":
-        raise MobaError(1, "the tensors must be on a CUDA device (got %s)" % device)
-    with torch.cuda.device(device):
-        _check(call(_stream(stream)))
+    cuda = torch.cuda
+    if stream is None:
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the address without a Stream object
+        stream = raw(index) if raw is not None else cuda.current_stream(index)
+    stream = getattr(stream, "cuda_stream", stream)
+    if cuda.current_device() == index:
+        rc = fn(*args, stream)
+    else:
+        with cuda.device(index):
+            rc = fn(*args, stream)
+    if rc != 0:
+        raise MobaError(rc, load().moba_last_error().decode())
 
 
 def moba_cache_tables(p: MobaCacheParams, add, lens, tables, free_pages, free_state, lens_out, free_state_out,
                       cu_new, slots, status, stream=None) -> None:
     """Block tables, slot map and free-page ring for the next step: add[s] new tokens for request s
     (0: none, negative: it ends).  lens_out may be lens, free_state_out may be free_state."""
-    p.check(add.device, add=add, lens=lens, tables=tables, free_pages=free_pages, free_state=free_state,
-            lens_out=lens_out, free_state_out=free_state_out, cu_new=cu_new, slots=slots, status=status)
-    _on(add.device, stream, lambda st: load().moba_cache_tables(
-        p.ref(), _ptr(add), _ptr(lens), _ptr(tables), _ptr(free_pages), _ptr(free_state), _ptr(lens_out),
-        _ptr(free_state_out), _ptr(cu_new), _ptr(slots), slots.shape[0], _ptr(status), st))
+    index = _on(add)
+    ptr = p._pointers(index, p._tables, (add, lens, tables, free_pages, free_state, lens_out, free_state_out, cu_new,
+                                         status))
+    _call(index, stream, load().moba_cache_tables, p._ref, *ptr[:8], p._slots(index, slots), slots.shape[0], ptr[8])
 
 
 def moba_cache_append(p: MobaCacheParams, K, V, cu_new, lens, slots, tables, Kc, Vc, Ks, Vs, Kbar,
                       stream=None) -> None:
     """Writes the new tokens K, V [n, Hkv, D] (rows any multiple of 8 elements apart) into their
     slots and pools the keys of blocks that become complete; lens are those after the step."""
-    p.check(K.device, K=K, V=V, cu_new=cu_new, lens=lens, slots=slots, tables=tables, Kc=Kc, Vc=Vc, Ks=Ks, Vs=Vs,
-            Kbar=Kbar)
+    index = _on(K)
+    row, strides = p.c.num_kv_heads * p.c.head_dim, []
     n = K.shape[0]
+    for name, t in (("K", K), ("V", V)):
+        dtype, shape = p.buffers[name]
+        size, stride = t.shape, t.stride()
+        if (t.dtype is not dtype or len(size) != 3 or size[1:] != shape[1:] or t.get_device() != index
+                or stride[1:] != (size[2], 1)):
+            p._check_one(name, t, index)
+        strides.append(stride[0] if n > 1 else row)
+    ptr = p._pointers(index, p._append, (cu_new, lens, tables, Kc, Vc, Ks, Vs, Kbar))
+    slot_ptr = p._slots(index, slots)
     if V.shape[0] != n or slots.shape[0] != n:
         raise MobaError(1, "K, V and slots must have the same number of tokens (got %d, %d, %d)"
                         % (n, V.shape[0], slots.shape[0]))
-    row = p.c.num_kv_heads * p.c.head_dim
-    ks, vs = (K.stride(0), V.stride(0)) if n > 1 else (row, row)
-    _on(K.device, stream, lambda st: load().moba_cache_append(
-        p.ref(), _ptr(K), ks, _ptr(V), vs, n, _ptr(cu_new), _ptr(lens), _ptr(slots), _ptr(tables), _ptr(Kc),
-        _ptr(Vc), _ptr(Ks), _ptr(Vs), _ptr(Kbar), st))
+    _call(index, stream, load().moba_cache_append, p._ref, K.data_ptr(), strides[0], V.data_ptr(), strides[1], n,
+          ptr[0], ptr[1], slot_ptr, *ptr[2:])
 
 
 def moba_cache_decode_workspace_size(p: MobaCacheParams) -> int:
@@ -413,14 +461,13 @@ def moba_cache_decode_fwd(p: MobaCacheParams, Q, Kc, Vc, Ks, Vs, Kbar, lens, tab
                           stream=None) -> None:
     """Gated decode: Q [max_seqs, Hq, D] (the newest token of each request) against the paged 8-bit
     cache; O [max_seqs, Hq, D], LSE [max_seqs, Hq], and sel [max_seqs, Hq, top_k] if given."""
-    p.check(Q.device, Q=Q, Kc=Kc, Vc=Vc, Ks=Ks, Vs=Vs, Kbar=Kbar, lens=lens, tables=tables, O=O, LSE=LSE)
-    if sel is not None:
-        p.check(Q.device, sel=sel)
-    if workspace.device != Q.device or not workspace.is_contiguous():
+    index = _on(Q)
+    ptr = p._pointers(index, p._decode, (Q, Kc, Vc, Ks, Vs, Kbar, lens, tables, O, LSE))
+    sel_ptr = p._pointers(index, p._sel, (sel,))[0] if sel is not None else None
+    if workspace.get_device() != index or not workspace.is_contiguous():
         raise MobaError(1, "workspace must be contiguous and on %s" % Q.device)
-    _on(Q.device, stream, lambda st: load().moba_cache_decode_fwd(
-        p.ref(), _ptr(Q), _ptr(Kc), _ptr(Vc), _ptr(Ks), _ptr(Vs), _ptr(Kbar), _ptr(lens), _ptr(tables), _ptr(sel),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(O), _ptr(LSE), st))
+    _call(index, stream, load().moba_cache_decode_fwd, p._ref, *ptr[:8], sel_ptr, workspace.data_ptr(),
+          workspace.numel() * workspace.element_size(), *ptr[8:])
 
 
 def alloc_cache_workspace(p: MobaCacheParams, device="cuda"):
@@ -443,7 +490,7 @@ class MobaCache:
 
         def zeros(name):
             dtype, shape = p.buffers[name]
-            return torch.zeros(shape, dtype=getattr(torch, dtype[6:]), device=self.device)
+            return torch.zeros(shape, dtype=dtype, device=self.device)
 
         self.Kc, self.Vc, self.Ks, self.Vs, self.Kbar = (zeros(n) for n in ("Kc", "Vc", "Ks", "Vs", "Kbar"))
         self.lens, self.tables, self.cu_new, self.status = (zeros(n) for n in ("lens", "tables", "cu_new", "status"))

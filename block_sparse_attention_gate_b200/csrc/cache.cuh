@@ -3,6 +3,8 @@
 
 #include <cuda_fp8.h>
 
+#include <atomic>
+
 #include "moba.h"
 
 #include "moba_internal.cuh"
@@ -90,6 +92,21 @@ struct CacheDecodeWork {
 };
 
 int cache_chunk_keys(const CacheGeom& g);
+// Raises a kernel's limit of dynamic shared memory, once for each device (a kernel takes the same
+// amount in every launch).
+template <auto kKernel>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};  // a bit for each device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 cudaError_t launch_cache_tables(const CacheGeom& g, const int32_t* add, const int32_t* lens, int32_t* tables,
                                 int32_t* free_pages, const int32_t* free_state, int32_t* lens_out,
                                 int32_t* free_state_out, int32_t* cu_new, int32_t* slots, int32_t max_tokens,

@@ -508,8 +508,7 @@ cudaError_t launch_prompt(const CacheGeom& g, const AppendSide& sk, const Append
   cfg.blockDim = dim3(prompt_threads(kPS));
   cfg.dynamicSmemBytes = (kAhead + 1) * kPS * kD * 2;
   cfg.stream = st;
-  auto kernel = cache_prompt_kernel<kD, kFmt, kPS, kAhead>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+  const cudaError_t e = allow_smem<cache_prompt_kernel<kD, kFmt, kPS, kAhead>>((int)cfg.dynamicSmemBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -517,7 +516,7 @@ cudaError_t launch_prompt(const CacheGeom& g, const AppendSide& sk, const Append
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, g, sk, sv, max_tokens, ranks, cu_new, lens, slots,
+  return cudaLaunchKernelEx(&cfg, cache_prompt_kernel<kD, kFmt, kPS, kAhead>, g, sk, sv, max_tokens, ranks, cu_new, lens, slots,
                             tables, Kbar);
 }
 

@@ -829,10 +829,8 @@ cudaError_t launch_decode_t(const CacheGeom& g, const __nv_bfloat16* Q, const ui
   CUtensorMap tk, tv;
   if ((e = make_codes_map(&tk, Kc, g)) != cudaSuccess) return e;
   if ((e = make_codes_map(&tv, Vc, g)) != cudaSuccess) return e;
-  auto attn = cache_attn_kernel<kD, kFmt>;
-  if ((e = cudaFuncSetAttribute(attn, cudaFuncAttributeMaxDynamicSharedMemorySize, AttnLayout<kD>::kAlloc)) != cudaSuccess)
-    return e;
-  e = launch_dependent(dim3((unsigned)sms), AttnLayout<kD>::kWarps * 32, AttnLayout<kD>::kAlloc, st, attn, tk, tv, g, Q, Ks, Vs,
+  if ((e = allow_smem<cache_attn_kernel<kD, kFmt>>(AttnLayout<kD>::kAlloc)) != cudaSuccess) return e;
+  e = launch_dependent(dim3((unsigned)sms), AttnLayout<kD>::kWarps * 32, AttnLayout<kD>::kAlloc, st, cache_attn_kernel<kD, kFmt>, tk, tv, g, Q, Ks, Vs,
                        lens, tables, w, g.B * g.Hkv * ((g.G + 7) / 8));
   if (e != cudaSuccess) return e;
   // many parts: all warps of a CTA on one row
