@@ -15,6 +15,8 @@
 #include <cudaTypedefs.h>
 #include <float.h>
 
+#include <type_traits>
+
 #include "cache.cuh"
 #include "sm100.cuh"
 
@@ -223,11 +225,11 @@ __global__ void __launch_bounds__(kGateWarps * 32)
 //    swizzled tiles by 16-byte reads without bank conflicts; only the weights change places between
 //    lanes (movmatrix).
 
-constexpr int kTile = 32;       // keys of a stage
 constexpr int kPiece = 256;     // keys whose pages a warp holds at a time (at most 16 pages)
 
 template <int kD>
 struct AttnLayout {
+  static constexpr int kTile = 32;                          // keys of a stage
   static constexpr int kWarps = kD == 64 ? 12 : 8;
   static constexpr int kStages = kD == 64 ? 4 : 3;
   static constexpr int kHalf = kTile * kD;                  // codes of K (or V) of a stage
@@ -307,7 +309,7 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
                       const __nv_bfloat16* __restrict__ Q, const float* __restrict__ Ks, const float* __restrict__ Vs,
                       const int32_t* __restrict__ lens, const int32_t* __restrict__ tables, CacheDecodeWork w, int NI) {
   using L = AttnLayout<kD>;
-  constexpr int kStages = L::kStages;
+  constexpr int kStages = L::kStages, kTile = L::kTile, kMT = kTile / 16;
   constexpr int kW = kD / 16;   // k steps of K Q^T = 16-row tiles of V^T
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -420,33 +422,37 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
   auto pages_of = [&](const Piece& p) -> int32_t {
     return lane << lps < p.n ? __ldg(tables + (size_t)p.s * g.MP + ((p.block * g.bs + p.key0) >> lps) + lane) : -1;
   };
-  // Bad pages become -1 and are reported; the others' scales are fetched.
-  auto look_at = [&](const Piece& p, int32_t& page, float& ks, float& vs) {
+  // Bad pages become -1 and are reported; the others' scales are fetched.  True if there are any.
+  auto look_at = [&](const Piece& p, int32_t& page, float& ks, float& vs) -> bool {
+    const bool bad = lane << lps < p.n && !page_ok(g, page);
     ks = 0.f, vs = 1.f;
     if (page_ok(g, page)) {
       ks = __ldg(Ks + (size_t)page * g.Hkv + p.gk);
       vs = __ldg(Vs + (size_t)page * g.Hkv + p.gk);
     } else {
-      if (lane << lps < p.n) atomicOr(g.err, kErrBadPage);
+      if (bad) atomicOr(g.err, kErrBadPage);
       page = -1;
     }
+    return __any_sync(0xffffffffu, bad);
   };
   const int box = min(g.ps, kTile);
   int wr = 0;  // stage that the next copy goes to
   auto issue = [&](const Piece& p, int32_t page, int tile) {
     uint8_t* dst = ring + wr * 2 * L::kHalf;
-    int32_t pg[2];
+    int32_t pg[kMT];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
+    for (int x = 0; x < kMT; ++x) {
       const int key = tile * kTile + x * box;
       pg[x] = __shfl_sync(0xffffffffu, page, key >> lps & 31);
       if (x * box >= kTile || key >= p.n) pg[x] = -1;
     }
     if (lane == 0) {
-      const uint32_t bytes = (uint32_t)((pg[0] >= 0) + (pg[1] >= 0)) * 2u * box * kD;
-      if (bytes) mbar_expect_tx(&full[wr], bytes); else mbar_arrive(&full[wr]);
+      uint32_t boxes = 0;
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+      for (int x = 0; x < kMT; ++x) boxes += pg[x] >= 0;
+      if (boxes) mbar_expect_tx(&full[wr], boxes * 2 * box * kD); else mbar_arrive(&full[wr]);
+#pragma unroll
+      for (int x = 0; x < kMT; ++x)
         if (pg[x] >= 0) {
           const int row = (p.key0 + tile * kTile + x * box) & (g.ps - 1), slab = pg[x] * g.Hkv + p.gk;
           tma_load_3d(dst + x * box * kD, &tmK, &full[wr], 0, row, slab);
@@ -463,7 +469,7 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
   advance(nxt, cur);
   int32_t page_c = pages_of(cur), page_n = -1;
   float ks, vs, ks_n = 0.f, vs_n = 1.f;
-  look_at(cur, page_c, ks, vs);
+  bool odd = look_at(cur, page_c, ks, vs), odd_n = false;
   int issued_c = 0, issued_n = 0, flying = 0;
   for (; issued_c < min(tiles_of(cur), kStages); ++issued_c, ++flying) issue(cur, page_c, issued_c);
   bool more = advance(cur, nxt), looked = false, ok = true;
@@ -517,24 +523,24 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
     }
     const float lvs = log2f(vs);
     const int tiles = tiles_of(cur);
-    for (int tile = 0; tile < tiles; ++tile) {
-      ok = mbar_wait_warp(&full[rd], parity, g.err);
-      if (!ok) break;
+    // One tile.  kOdd: some of its keys do not count (behind the newest token, or on a bad page).
+    auto take = [&](auto odd_tile, int tile) {
+      constexpr bool kOdd = decltype(odd_tile)::value;
       const uint8_t* kst = ring + rd * 2 * L::kHalf;
       const uint8_t* vst = kst + L::kHalf;
-      float z[2][4];
+      float c[kMT][4];
       // ---- S = K Q^T: keys gq and gq + 8 of each 16, heads 2t and 2t + 1
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
+      for (int mt = 0; mt < kMT; ++mt) {
         uint32_t kw[2][kW];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int r = mt * 16 + x * 8 + gq;
           if constexpr (kD == 128) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const uint4 v = *reinterpret_cast<const uint4*>(kst + r * 128 + (((2 * t + c) ^ (r & 7)) << 4));
-              kw[x][4 * c] = v.x, kw[x][4 * c + 1] = v.y, kw[x][4 * c + 2] = v.z, kw[x][4 * c + 3] = v.w;
+            for (int h = 0; h < 2; ++h) {
+              const uint4 v = *reinterpret_cast<const uint4*>(kst + r * 128 + (((2 * t + h) ^ (r & 7)) << 4));
+              kw[x][4 * h] = v.x, kw[x][4 * h + 1] = v.y, kw[x][4 * h + 2] = v.z, kw[x][4 * h + 3] = v.w;
             }
           } else {
             const uint4 v = *reinterpret_cast<const uint4*>(kst + r * 64 + ((t ^ ((r >> 1) & 3)) << 4));
@@ -549,39 +555,61 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
                   qb[j][1]);
         }
 #pragma unroll
-        for (int x = 0; x < 4; ++x) z[mt][x] = c0[x] + c1[x];
+        for (int x = 0; x < 4; ++x) c[mt][x] = c0[x] + c1[x];
       }
-      // ---- online softmax
-      int live[2];     // keys of each 16 that count
-      float zw[2][4];  // with the value scale
-      float mx0 = m[0], mx1 = m[1];
+      // the values are fetched ahead of their use
+      uint32_t v[kMT][4][kW / 2];  // keys 2t, 2t + 1, 2t + 8, 2t + 9 of each 16
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        const int key = tile * kTile + mt * 16, pi = key >> lps & 31;
-        const float k1 = __shfl_sync(0xffffffffu, ks, pi), lv = __shfl_sync(0xffffffffu, lvs, pi);
-        const int32_t pg = __shfl_sync(0xffffffffu, page_c, pi);
-        live[mt] = pg >= 0 ? min(16, cur.n - key) : 0;
-        z[mt][0] *= k1 * sf[0];
-        z[mt][1] *= k1 * sf[1];
-        z[mt][2] *= k1 * sf[0];
-        z[mt][3] *= k1 * sf[1];
-        if (live[mt] < 16) {
-          if (gq >= live[mt]) z[mt][0] = z[mt][1] = -INFINITY;
-          if (gq + 8 >= live[mt]) z[mt][2] = z[mt][3] = -INFINITY;
+      for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int r = mt * 16 + 2 * t + (x & 1) + 8 * (x >> 1);
+          if constexpr (kD == 128) {
+            const uint4 u = *reinterpret_cast<const uint4*>(vst + r * 128 + ((gq ^ (r & 7)) << 4));
+            v[mt][x][0] = u.x, v[mt][x][1] = u.y, v[mt][x][2] = u.z, v[mt][x][3] = u.w;
+          } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(vst + r * 64 + (((gq >> 1) ^ ((r >> 1) & 3)) << 4) + (gq & 1) * 8);
+            v[mt][x][0] = u.x, v[mt][x][1] = u.y;
+          }
         }
+      // ---- online softmax: z = c * f, and with the value scale z + lv
+      int live[kMT] = {};  // keys of each 16 that count
+      float f0[kMT], f1[kMT], lv[kMT], mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) zw[mt][x] = z[mt][x] + lv;
-        mx0 = max3(mx0, zw[mt][0], zw[mt][2]);
-        mx1 = max3(mx1, zw[mt][1], zw[mt][3]);
+      for (int mt = 0; mt < kMT; ++mt) {
+        const int key = tile * kTile + mt * 16, pi = key >> lps & 31;
+        const float k1 = __shfl_sync(0xffffffffu, ks, pi);
+        lv[mt] = __shfl_sync(0xffffffffu, lvs, pi);
+        f0[mt] = k1 * sf[0];
+        f1[mt] = k1 * sf[1];
+        if constexpr (kOdd) {
+          const int32_t pg = __shfl_sync(0xffffffffu, page_c, pi);
+          live[mt] = pg >= 0 ? min(16, cur.n - key) : 0;
+        }
       }
+      auto masked = [&](int mt, int x) { return kOdd && (x < 2 ? gq : gq + 8) >= live[mt]; };
+      // c * f, plus what is added to it; -inf for a masked key
+      auto score = [&](int mt, int x, float plus) {
+        const float v = fmaf(c[mt][x], x & 1 ? f1[mt] : f0[mt], plus);
+        return masked(mt, x) ? -INFINITY : v;
+      };
 #pragma unroll
-      for (int off = 4; off <= 16; off <<= 1) {
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
+      for (int mt = 0; mt < kMT; ++mt) {
+        mx0 = max3(mx0, score(mt, 0, lv[mt]), score(mt, 2, lv[mt]));
+        mx1 = max3(mx1, score(mt, 1, lv[mt]), score(mt, 3, lv[mt]));
       }
-      const float b0 = mx0 == -INFINITY ? 0.f : mx0, b1 = mx1 == -INFINITY ? 0.f : mx1;
-      if (__any_sync(0xffffffffu, mx0 != m[0] || mx1 != m[1])) {
-        const float a0 = ex2(m[0] - b0), a1 = ex2(m[1] - b1);
+      // m is a maximum of earlier keys, not the largest so far: weights up to 2^kSlack are as good in fp16
+      // and fp32, and the exact maximum over the lanes is only needed when a key leaves that range
+      constexpr float kSlack = 8.f;
+      if (__any_sync(0xffffffffu, mx0 > m[0] + kSlack || mx1 > m[1] + kSlack)) {
+#pragma unroll
+        for (int off = 4; off <= 16; off <<= 1) {
+          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
+          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
+        }
+        mx0 = fmaxf(mx0, m[0]);
+        mx1 = fmaxf(mx1, m[1]);
+        const float a0 = mx0 == -INFINITY ? 0.f : ex2(m[0] - mx0), a1 = mx1 == -INFINITY ? 0.f : ex2(m[1] - mx1);
         l[0] *= a0;
         l[1] *= a1;
 #pragma unroll
@@ -594,42 +622,43 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
         m[0] = mx0;
         m[1] = mx1;
       }
+      const float b0 = m[0] == -INFINITY ? 0.f : m[0], b1 = m[1] == -INFINITY ? 0.f : m[1];
       // ---- O += V^T P: dimensions of group gq, heads 2t and 2t + 1
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        l[0] += ex2(z[mt][0] - b0) + ex2(z[mt][2] - b0);
-        l[1] += ex2(z[mt][1] - b1) + ex2(z[mt][3] - b1);
-        const uint32_t p0 = transpose8(pack_half2(ex2(zw[mt][0] - b0), ex2(zw[mt][1] - b1)));
-        const uint32_t p1 = transpose8(pack_half2(ex2(zw[mt][2] - b0), ex2(zw[mt][3] - b1)));
-        uint32_t v[4][kW / 2];  // keys 2t, 2t + 1, 2t + 8, 2t + 9
+      for (int mt = 0; mt < kMT; ++mt) {
+        l[0] += ex2(score(mt, 0, -b0)) + ex2(score(mt, 2, -b0));
+        l[1] += ex2(score(mt, 1, -b1)) + ex2(score(mt, 3, -b1));
+        const float w0 = lv[mt] - b0, w1 = lv[mt] - b1;
+        const uint32_t p0 = transpose8(pack_half2(ex2(score(mt, 0, w0)), ex2(score(mt, 1, w1))));
+        const uint32_t p1 = transpose8(pack_half2(ex2(score(mt, 2, w0)), ex2(score(mt, 3, w1))));
+        if constexpr (kOdd) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int kk = 2 * t + (x & 1) + 8 * (x >> 1), r = mt * 16 + kk;
-          if constexpr (kD == 128) {
-            const uint4 u = *reinterpret_cast<const uint4*>(vst + r * 128 + ((gq ^ (r & 7)) << 4));
-            v[x][0] = u.x, v[x][1] = u.y, v[x][2] = u.z, v[x][3] = u.w;
-          } else {
-            const uint2 u = *reinterpret_cast<const uint2*>(vst + r * 64 + (((gq >> 1) ^ ((r >> 1) & 3)) << 4) + (gq & 1) * 8);
-            v[x][0] = u.x, v[x][1] = u.y;
-          }
-          if (live[mt] < 16 && kk >= live[mt])  // whatever stands there must not meet a weight of 0
+          for (int x = 0; x < 4; ++x)
+            if (2 * t + (x & 1) + 8 * (x >> 1) >= live[mt]) {  // whatever stands there must not meet a weight of 0
 #pragma unroll
-            for (int j = 0; j < kW / 2; ++j) v[x][j] = 0;
+              for (int j = 0; j < kW / 2; ++j) v[mt][x][j] = 0;
+            }
         }
 #pragma unroll
         for (int j = 0; j < kW / 2; ++j) {
-          const uint32_t a = ready<kFmt>(v[0][j]), b = ready<kFmt>(v[1][j]), c = ready<kFmt>(v[2][j]), d = ready<kFmt>(v[3][j]);
-          const uint32_t x0 = prmt(a, b, 0x5140), x1 = prmt(a, b, 0x7362), y0 = prmt(c, d, 0x5140), y1 = prmt(c, d, 0x7362);
+          const uint32_t a = ready<kFmt>(v[mt][0][j]), b = ready<kFmt>(v[mt][1][j]);
+          const uint32_t d = ready<kFmt>(v[mt][2][j]), e = ready<kFmt>(v[mt][3][j]);
+          const uint32_t x0 = prmt(a, b, 0x5140), x1 = prmt(a, b, 0x7362), y0 = prmt(d, e, 0x5140), y1 = prmt(d, e, 0x7362);
           mma_f16(o[2 * j], half2_lo<kFmt>(x0), half2_hi<kFmt>(x0), half2_lo<kFmt>(y0), half2_hi<kFmt>(y0), p0, p1);
           mma_f16(o[2 * j + 1], half2_lo<kFmt>(x1), half2_hi<kFmt>(x1), half2_lo<kFmt>(y1), half2_hi<kFmt>(y1), p0, p1);
         }
       }
+    };
+    for (int tile = 0; tile < tiles; ++tile) {
+      ok = mbar_wait_warp(&full[rd], parity, g.err);
+      if (!ok) break;
+      if (odd || (tile + 1) * kTile > cur.n) take(std::true_type{}, tile); else take(std::false_type{}, tile);
       __syncwarp();  // the stage is read
       if (++rd == kStages) rd = 0, parity ^= 1;
       --flying;
       if (issued_c < tiles) issue(cur, page_c, issued_c++), ++flying;
       else if (more) {
-        if (!looked) look_at(nxt, page_n, ks_n, vs_n), looked = true;
+        if (!looked) odd_n = look_at(nxt, page_n, ks_n, vs_n), looked = true;
         if (issued_n < tiles_of(nxt)) issue(nxt, page_n, issued_n++), ++flying;
       }
     }
@@ -657,8 +686,9 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
       }
     }
     if (!more) break;
-    if (!looked) look_at(nxt, page_n, ks_n, vs_n);
+    if (!looked) odd_n = look_at(nxt, page_n, ks_n, vs_n);
     cur = nxt;
+    odd = odd_n;
     page_c = page_n;
     ks = ks_n;
     vs = vs_n;
@@ -759,9 +789,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
 
 // ---------------------------------------------------------------------------------- launch
 
-// Codes [P * Hkv, ps, D] as dims (d, row, slab); boxes of D x min(ps, kTile) x 1, swizzled over the
+// Codes [P * Hkv, ps, D] as dims (d, row, slab); boxes of D x min(ps, tile) x 1, swizzled over the
 // whole row (128 or 64 bytes).
-cudaError_t make_codes_map(CUtensorMap* m, const void* base, const CacheGeom& g) {
+cudaError_t make_codes_map(CUtensorMap* m, const void* base, const CacheGeom& g, int tile) {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   if (!fn) {
     void* p = nullptr;
@@ -773,7 +803,7 @@ cudaError_t make_codes_map(CUtensorMap* m, const void* base, const CacheGeom& g)
   }
   const cuuint64_t dims[3] = {(cuuint64_t)g.D, (cuuint64_t)g.ps, (cuuint64_t)g.P * g.Hkv};
   const cuuint64_t strides[2] = {(cuuint64_t)g.D, (cuuint64_t)g.D * g.ps};
-  const cuuint32_t box[3] = {(cuuint32_t)g.D, (cuuint32_t)(g.ps < kTile ? g.ps : kTile), 1};
+  const cuuint32_t box[3] = {(cuuint32_t)g.D, (cuuint32_t)(g.ps < tile ? g.ps : tile), 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -827,8 +857,8 @@ cudaError_t launch_decode_t(const CacheGeom& g, const __nv_bfloat16* Q, const ui
                              : launch_gate<kD, 4>(g, Q, Kbar, lens, sel, w, st);
   if (e != cudaSuccess) return e;
   CUtensorMap tk, tv;
-  if ((e = make_codes_map(&tk, Kc, g)) != cudaSuccess) return e;
-  if ((e = make_codes_map(&tv, Vc, g)) != cudaSuccess) return e;
+  if ((e = make_codes_map(&tk, Kc, g, AttnLayout<kD>::kTile)) != cudaSuccess) return e;
+  if ((e = make_codes_map(&tv, Vc, g, AttnLayout<kD>::kTile)) != cudaSuccess) return e;
   if ((e = allow_smem<cache_attn_kernel<kD, kFmt>>(AttnLayout<kD>::kAlloc)) != cudaSuccess) return e;
   e = launch_dependent(dim3((unsigned)sms), AttnLayout<kD>::kWarps * 32, AttnLayout<kD>::kAlloc, st, cache_attn_kernel<kD, kFmt>, tk, tv, g, Q, Ks, Vs,
                        lens, tables, w, g.B * g.Hkv * ((g.G + 7) / 8));
@@ -844,14 +874,20 @@ cudaError_t launch_decode_t(const CacheGeom& g, const __nv_bfloat16* Q, const ui
 
 }  // namespace
 
-// Keys of a unit, a power of two so that the pieces of every unit start on a page: the longest that
-// leaves every warp four units if all heads of a group agree (more where they do not), at least 128.
-// Longer ones write and merge fewer partial rows, shorter ones leave less to the slowest warp.
+// Keys of a unit, a power of two from 128 on so that the pieces of every unit start on a page: the
+// longest that leaves enough units for each warp, as a unit costs a warp about as much as 40 keys.
+// Units are counted as if half of a group's heads shared their choices.  With more blocks than warps, 3
+// units a warp keep their shares even: 64 caches of 128K take 388 us at 1024 keys, 408 at 256 (32/8 heads
+// of 128, top_k 3 of blocks of 2048); 37 ragged ones of 64 dimensions 57 us at 256, 64 at 512 (blocks of
+// 512).  With fewer, a bit more than half as many units as warps have enough copies on their way to fill
+// the memory: eight caches of 128K take 60 us at 1024 keys, 66 at 256; one of 1M 28 us at 128, 38 at 512.
 int cache_chunk_keys(const CacheGeom& g) {
-  const int64_t rows = (int64_t)g.B * g.Hkv * ((g.G + 7) / 8) * g.k;
+  const int64_t entries = (int64_t)g.B * g.Hkv * ((g.G + 7) / 8);
+  const int64_t past = (g.k - 1) * (1 + (g.G < 8 ? g.G : 8)) / 2, blocks = entries * (1 + (past < g.MB - 1 ? past : g.MB - 1));
   const int64_t warps = 148 * (g.D == 64 ? AttnLayout<64>::kWarps : AttnLayout<128>::kWarps);
+  const int64_t want = blocks >= warps ? 3 * warps : warps * 3 / 5;
   int ck = 8192;
-  while (ck > 128 && (ck / 2 >= g.bs || rows * ((g.bs + ck - 1) / ck) < 4 * warps)) ck /= 2;
+  while (ck > 128 && (ck / 2 >= g.bs || blocks * ((g.bs + ck - 1) / ck) < want)) ck /= 2;
   return ck;
 }
 
