@@ -32,7 +32,7 @@ constexpr float kLn2C = 0.6931471805599453f;
 
 constexpr int kGateWarps = 8;
 constexpr int kGateRows = 8;   // blocks that a warp scores at a time
-constexpr int kHeld = 8;       // scores that a lane holds while a head's best are picked
+constexpr int kHeld = 16;      // scores that a lane holds while a head's best are picked
 
 // Order of scores as unsigned numbers: NaN last, -0 as +0.  No score maps to 0.
 __device__ __forceinline__ uint64_t score_key(double x) {
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kGateWarps * 32)
     cache_gate_kernel(CacheGeom g, const __nv_bfloat16* __restrict__ Q, const float* __restrict__ Kbar,
                       const int32_t* __restrict__ lens, int32_t* __restrict__ sel, CacheDecodeWork w) {
   constexpr int kDL = kD / 32;
-  __shared__ int32_t s_sel[8][kMaxTopK];
+  __shared__ int32_t s_sel[8][kMaxTopK], s_first[kGateWarps];
   const int rank = blockIdx.x, gk = blockIdx.y, s = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   launch_dependents();  // the attention kernel may be set up meanwhile
@@ -174,33 +174,37 @@ __global__ void __launch_bounds__(kGateWarps * 32)
       }
     }
     __syncthreads();
-    if (warp == 0) {
-      const size_t idx = ((size_t)s * g.Hkv + gk) * HT + ht;
-      CacheSeg* segs = w.segs + idx * w.max_segs;
-      int count = 0;
-      const int n = heads * m;  // chosen (head, slot) pairs, head by head
-      for (int e0 = 0; e0 < n; e0 += 32) {
-        const int e = e0 + lane, eh = e / m, ej = 1 + e - eh * m;
-        const int32_t b = e < n ? s_sel[eh][ej] : -1;
-        bool first = e < n;
-        CacheSeg seg{b, g.bs, {~0u, ~0u}};
-        for (int oh = 0; oh < heads; ++oh)
-          for (int oj = 1; oj <= m; ++oj)
-            if (e < n && s_sel[oh][oj] == b) {
-              if (oh < eh) first = false;  // a head chooses a block once
-              const uint32_t keep = ~(0xffu << 8 * (oh & 3)), put = (uint32_t)oj << 8 * (oh & 3);
-              if (oh < 4) seg.slots[0] = (seg.slots[0] & keep) | put; else seg.slots[1] = (seg.slots[1] & keep) | put;
-            }
-        const uint32_t firsts = __ballot_sync(0xffffffffu, first);
-        if (first) segs[count + __popc(firsts & ((1u << lane) - 1))] = seg;
-        count += __popc(firsts);
-      }
-      if (lane == 0) {  // last the own block, every head's slot 0; heads beyond the group take nothing
-        CacheSeg own{i, len - max(i, 0) * g.bs, {~0u, ~0u}};
-        for (int h = 0; h < heads; ++h) own.slots[h >> 2] &= ~(0xffu << 8 * (h & 3));
-        if (i >= 0) segs[count] = own;
-        w.units[idx] = count * w.NC + (own.keys + w.CK - 1) / w.CK;  // 0 where the request is empty
-      }
+    // a thread for each chosen (head, slot) pair, head by head: the first pair with a block describes it
+    const size_t idx = ((size_t)s * g.Hkv + gk) * HT + ht;
+    CacheSeg* segs = w.segs + idx * w.max_segs;
+    const int e = threadIdx.x, eh = m > 0 ? e / m : 8, ej = 1 + e - eh * m;
+    bool first = eh < heads;
+    CacheSeg seg{0, g.bs, {~0u, ~0u}};
+    if (first) {
+      seg.block = s_sel[eh][ej];
+      for (int oh = 0; oh < heads; ++oh)
+        for (int oj = 1; oj <= m; ++oj)
+          if (s_sel[oh][oj] == seg.block) {
+            if (oh < eh) first = false;  // a head chooses a block once
+            const uint32_t keep = ~(0xffu << 8 * (oh & 3)), put = (uint32_t)oj << 8 * (oh & 3);
+            if (oh < 4) seg.slots[0] = (seg.slots[0] & keep) | put; else seg.slots[1] = (seg.slots[1] & keep) | put;
+          }
+    }
+    const uint32_t firsts = __ballot_sync(0xffffffffu, first);
+    if (lane == 0) s_first[warp] = __popc(firsts);
+    __syncthreads();
+    int at = __popc(firsts & ((1u << lane) - 1)), count = 0;
+#pragma unroll
+    for (int x = 0; x < kGateWarps; ++x) {
+      if (x < warp) at += s_first[x];
+      count += s_first[x];
+    }
+    if (first) segs[at] = seg;
+    if (threadIdx.x == 0) {  // last the own block, every head's slot 0; heads beyond the group take nothing
+      CacheSeg own{i, len - max(i, 0) * g.bs, {~0u, ~0u}};
+      for (int h = 0; h < heads; ++h) own.slots[h >> 2] &= ~(0xffu << 8 * (h & 3));
+      if (i >= 0) segs[count] = own;
+      w.units[idx] = count * w.NC + (own.keys + w.CK - 1) / w.CK;  // 0 where the request is empty
     }
     __syncthreads();
   }
@@ -708,7 +712,8 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
 
 // Partial results of a (request, head), merged by online softmax (log2 units) by kWarps warps: warp x
 // takes every kWarps-th part.
-constexpr int kMergeWarps = 4;  // of a CTA
+constexpr int kMergeWarps = 8;  // of a CTA
+constexpr int kMergeRows = 8;   // partial rows of a warp on their way at a time
 
 template <int kD, int kWarps>
 __global__ void __launch_bounds__(kMergeWarps * 32)
@@ -722,31 +727,16 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   const int32_t len = live ? cached_len(g, lens, (int)(row / g.Hq)) : 0;
   const int own = len > 0 ? (len - 1) / g.bs : 0, own_chunks = (len - own * g.bs + w.CK - 1) / w.CK;
   const int n = own_chunks + min(g.k - 1, own) * w.NC;  // slots are filled from the front
+  const int mine = n > part ? (n - part + kWarps - 1) / kWarps : 0;  // parts of this warp
   const float2* ml = w.part_ml + row * g.k * w.NC;
   const float* po = w.part_o + row * g.k * w.NC * kD + lane * kDL;
   auto at = [&](int x) { return x < own_chunks ? x : w.NC + (x - own_chunks); };
-  wait_for_primary();
-  float M = -INFINITY;
-  for (int x = lane; x < n; x += 32) M = fmaxf(M, __ldcg(ml + at(x)).x);
+  float f[kMergeRows][kDL];
+  auto fetch = [&](int x1) {  // this warp's rows [x1, x1 + kMergeRows)
 #pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  const float base = M == -INFINITY ? 0.f : M;
-  float L = 0.f, acc[kDL];
-#pragma unroll
-  for (int d = 0; d < kDL; ++d) acc[d] = 0.f;
-  const int mine = n > part ? (n - part + kWarps - 1) / kWarps : 0;  // parts of this warp
-  for (int x0 = 0; x0 < mine; x0 += 32) {
-    float wt = 0.f;
-    if (x0 + lane < mine) {
-      const float2 v = __ldcg(ml + at(part + (x0 + lane) * kWarps));
-      wt = ex2(v.x - base);
-      L = fmaf(v.y, wt, L);
-    }
-    for (int x1 = x0; x1 < min(mine, x0 + 32); x1 += 8) {  // 8 rows on their way at a time
-      float f[8][kDL];
-#pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const float* src = po + (size_t)at(part + min(x1 + x, mine - 1) * kWarps) * kD;
+    for (int x = 0; x < kMergeRows; ++x)
+      if (x1 + x < mine) {
+        const float* src = po + (size_t)at(part + (x1 + x) * kWarps) * kD;
         if constexpr (kDL == 4) {
           const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
           f[x][0] = v.x, f[x][1] = v.y, f[x][2] = v.z, f[x][3] = v.w;
@@ -755,8 +745,28 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
           f[x][0] = v.x, f[x][1] = v.y;
         }
       }
+  };
+  wait_for_primary();
+  fetch(0);  // while the weights are found
+  float M = -INFINITY;
+  for (int x = lane; x < n; x += 32) M = fmaxf(M, __ldcg(ml + at(x)).x);
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
+  for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  const float base = M == -INFINITY ? 0.f : M;
+  float L = 0.f, acc[kDL];
+#pragma unroll
+  for (int d = 0; d < kDL; ++d) acc[d] = 0.f;
+  for (int x0 = 0; x0 < mine; x0 += 32) {
+    float wt = 0.f;
+    if (x0 + lane < mine) {
+      const float2 v = __ldcg(ml + at(part + (x0 + lane) * kWarps));
+      wt = ex2(v.x - base);
+      L = fmaf(v.y, wt, L);
+    }
+    for (int x1 = x0; x1 < min(mine, x0 + 32); x1 += kMergeRows) {
+      if (x1 > 0) fetch(x1);
+#pragma unroll
+      for (int x = 0; x < kMergeRows; ++x) {
         const float wx = __shfl_sync(0xffffffffu, wt, (x1 + x) & 31);
         if (x1 + x < mine)
 #pragma unroll
@@ -863,7 +873,7 @@ cudaError_t launch_decode_t(const CacheGeom& g, const __nv_bfloat16* Q, const ui
   e = launch_dependent(dim3((unsigned)sms), AttnLayout<kD>::kWarps * 32, AttnLayout<kD>::kAlloc, st, cache_attn_kernel<kD, kFmt>, tk, tv, g, Q, Ks, Vs,
                        lens, tables, w, g.B * g.Hkv * ((g.G + 7) / 8));
   if (e != cudaSuccess) return e;
-  // many parts: all warps of a CTA on one row
+  // many parts: all warps of a CTA on one row (a warp has eight rows on their way at a time)
   const int64_t rows = (int64_t)g.B * g.Hq;
   if (g.k * w.NC > 8)
     return launch_dependent(dim3((unsigned)rows), kMergeWarps * 32, 0, st, cache_merge_kernel<kD, kMergeWarps>, g, lens, w,
