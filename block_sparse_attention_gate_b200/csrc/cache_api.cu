@@ -28,6 +28,12 @@ moba_status fail(moba_status st, const char* fmt, ...) {
 
 constexpr int64_t kI32Max = 2147483647LL;
 
+// Distinct blocks that a tile of 8 heads can choose.
+int cache_max_segs(const moba::CacheGeom& g) {
+  const int past = (g.G < 8 ? g.G : 8) * (g.k - 1);
+  return 1 + (past < g.MB - 1 ? past : g.MB - 1);
+}
+
 // Validate the parameters and derive the kernels' geometry (host only).
 moba_status make_cache_geom(const moba_cache_params* p, moba::CacheGeom* g) {
   if (!p) return fail(MOBA_ERR_INVALID_ARG, "params is NULL");
@@ -79,8 +85,7 @@ moba_status make_cache_geom(const moba_cache_params* p, moba::CacheGeom* g) {
   g->scale_log2 = g->scale * 1.4426950408889634f;
   g->err = nullptr;
   const int ck = moba::cache_chunk_keys(*g);
-  const int64_t past = MB - 1 < 8 * (p->top_k - 1) ? MB - 1 : 8 * (p->top_k - 1);
-  if ((1 + past) * ((p->block_size + ck - 1) / ck) * p->max_seqs * p->num_kv_heads * ((g->G + 7) / 8) > kI32Max)
+  if ((int64_t)cache_max_segs(*g) * ((p->block_size + ck - 1) / ck) * p->max_seqs * p->num_kv_heads * ((g->G + 7) / 8) > kI32Max)
     return fail(MOBA_ERR_UNSUPPORTED, "more than 2^31-1 chunks of chosen blocks");
   return MOBA_OK;
 }
@@ -101,8 +106,7 @@ moba::CacheDecodeWork carve_cache_decode(const moba::CacheGeom& g, char* base) {
   moba::CacheDecodeWork w;
   w.CK = moba::cache_chunk_keys(g);
   w.NC = (g.bs + w.CK - 1) / w.CK;
-  const int past = 8 * (g.k - 1);  // distinct earlier blocks that 8 heads can choose
-  w.max_segs = 1 + (past < g.MB - 1 ? past : g.MB - 1);
+  w.max_segs = cache_max_segs(g);
   const size_t rows = (size_t)g.B * g.Hq, parts = rows * g.k * w.NC;
   const size_t entries = (size_t)g.B * g.Hkv * ((g.G + 7) / 8);
   w.score = (uint64_t*)take(g.k > 1 ? rows * g.MB * sizeof(uint64_t) : 0);

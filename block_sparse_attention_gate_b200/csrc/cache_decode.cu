@@ -332,49 +332,59 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
   launch_dependents();
   wait_for_primary();  // the gate's results
 
-  // ---- units before each group of `per` entries of the work list
-  const int per = (NI + L::kMaxPrefix - 1) / L::kMaxPrefix, groups = (NI + per - 1) / per;
-  constexpr int kEach = L::kMaxPrefix / (L::kWarps * 32);
-  int32_t cnt[kEach], sum = 0;
-#pragma unroll
-  for (int x = 0; x < kEach; ++x) {
-    const int gr = threadIdx.x * kEach + x;
-    cnt[x] = 0;
-    if (gr < groups)
-      for (int y = gr * per; y < min(NI, (gr + 1) * per); ++y) cnt[x] += __ldcg(w.units + y);
-    sum += cnt[x];
-  }
-  int32_t inc = sum;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int32_t o = __shfl_up_sync(0xffffffffu, inc, off);
-    if (lane >= off) inc += o;
-  }
-  if (lane == 31) wsum[warp] = inc;
-  __syncthreads();
-  int32_t before = inc - sum;
-  for (int q = 0; q < warp; ++q) before += wsum[q];
-#pragma unroll
-  for (int x = 0; x < kEach; ++x) {
-    prefix[threadIdx.x * kEach + x] = before;
-    before += cnt[x];
-  }
-  if (threadIdx.x == L::kWarps * 32 - 1) prefix[L::kMaxPrefix] = before;
-  __syncthreads();
-  const int32_t total = prefix[L::kMaxPrefix];
-  const int64_t W = (int64_t)gridDim.x * L::kWarps, wid = (int64_t)blockIdx.x * L::kWarps + warp;
-  int32_t todo = (int32_t)((wid + 1) * total / W) - (int32_t)(wid * total / W);  // units of this warp
-  if (todo == 0) return;
-
-  // ---- work ahead: the description of the unit after the next piece is on its way while that piece's
-  // pages are, so that none of these loads is waited for
-  int n_idx, n_unit;  // the next unit to be opened
+  int32_t todo;       // units of this warp that are not opened yet
+  int n_idx, n_unit;  // the next of them
   int4 n_seg = make_int4(0, 0, 0, 0);
-  auto units_of = [&](int idx) { return per == 1 ? prefix[idx + 1] - prefix[idx] : __ldcg(w.units + idx); };
   auto fetch_seg = [&]() {
     n_seg = __ldcg(reinterpret_cast<const int4*>(w.segs + (size_t)n_idx * w.max_segs + n_unit / w.NC));
   };
-  {
+  const int64_t W = (int64_t)gridDim.x * L::kWarps, wid = (int64_t)blockIdx.x * L::kWarps + warp;
+  const int per = (NI + L::kMaxPrefix - 1) / L::kMaxPrefix, groups = (NI + per - 1) / per;
+  auto units_of = [&](int idx) { return per == 1 ? prefix[idx + 1] - prefix[idx] : __ldcg(w.units + idx); };
+  // ---- which units: where there is a warp for every one that an entry can have, each warp (spread over
+  // the SMs) looks at its own; else the warps take equal runs of those that there are
+  const int most = w.max_segs * w.NC;
+  if ((int64_t)NI * most <= W) {
+    __syncwarp();  // the barriers
+    const int u = warp * (int)gridDim.x + (int)blockIdx.x;
+    n_idx = u / most;
+    n_unit = u - n_idx * most;
+    if (n_idx >= NI) return;
+    fetch_seg();
+    todo = n_unit < __ldcg(w.units + n_idx);
+    if (todo == 0) return;
+  } else {
+    // units before each group of `per` entries
+    constexpr int kEach = L::kMaxPrefix / (L::kWarps * 32);
+    int32_t cnt[kEach], sum = 0;
+#pragma unroll
+    for (int x = 0; x < kEach; ++x) {
+      const int gr = threadIdx.x * kEach + x;
+      cnt[x] = 0;
+      if (gr < groups)
+        for (int y = gr * per; y < min(NI, (gr + 1) * per); ++y) cnt[x] += __ldcg(w.units + y);
+      sum += cnt[x];
+    }
+    int32_t inc = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int32_t o = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += o;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    int32_t before = inc - sum;
+    for (int q = 0; q < warp; ++q) before += wsum[q];
+#pragma unroll
+    for (int x = 0; x < kEach; ++x) {
+      prefix[threadIdx.x * kEach + x] = before;
+      before += cnt[x];
+    }
+    if (threadIdx.x == L::kWarps * 32 - 1) prefix[L::kMaxPrefix] = before;
+    __syncthreads();
+    const int32_t total = prefix[L::kMaxPrefix];
+    todo = (int32_t)((wid + 1) * total / W) - (int32_t)(wid * total / W);
+    if (todo == 0) return;
     const int32_t u = (int32_t)(wid * total / W);
     int lo = 0, hi = groups - 1;
     while (lo < hi) {
@@ -386,6 +396,9 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
     for (int32_t c; n_unit >= (c = units_of(n_idx));) n_unit -= c, ++n_idx;
     fetch_seg();
   }
+
+  // ---- work ahead: the description of the unit after the next piece is on its way while that piece's
+  // pages are, so that none of these loads is waited for
   // The piece after p into o (p: the last one, or idx -1); false behind the warp's last one.
   auto advance = [&](const Piece& p, Piece& o) -> bool {
     if (p.left > 0) {
@@ -422,13 +435,15 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
     return true;
   };
   const int lps = 31 - __clz(g.ps);
-  // Page of the lane-th run of ps keys (-1: none), not yet looked at.
+  // Keys of a piece are counted from the start of its first page (offset_of keys before its own first).
+  auto offset_of = [&](const Piece& p) { return p.key0 & (g.ps - 1); };
+  // The lane-th page of a piece (-1: none), not yet looked at.
   auto pages_of = [&](const Piece& p) -> int32_t {
-    return lane << lps < p.n ? __ldg(tables + (size_t)p.s * g.MP + ((p.block * g.bs + p.key0) >> lps) + lane) : -1;
+    return lane << lps < offset_of(p) + p.n ? __ldg(tables + (size_t)p.s * g.MP + ((p.block * g.bs + p.key0) >> lps) + lane) : -1;
   };
   // Bad pages become -1 and are reported; the others' scales are fetched.  True if there are any.
   auto look_at = [&](const Piece& p, int32_t& page, float& ks, float& vs) -> bool {
-    const bool bad = lane << lps < p.n && !page_ok(g, page);
+    const bool bad = lane << lps < offset_of(p) + p.n && !page_ok(g, page);
     ks = 0.f, vs = 1.f;
     if (page_ok(g, page)) {
       ks = __ldg(Ks + (size_t)page * g.Hkv + p.gk);
@@ -447,7 +462,7 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
 #pragma unroll
     for (int x = 0; x < kMT; ++x) {
       const int key = tile * kTile + x * box;
-      pg[x] = __shfl_sync(0xffffffffu, page, key >> lps & 31);
+      pg[x] = __shfl_sync(0xffffffffu, page, (offset_of(p) + key) >> lps & 31);
       if (x * box >= kTile || key >= p.n) pg[x] = -1;
     }
     if (lane == 0) {
@@ -581,7 +596,7 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
       float f0[kMT], f1[kMT], lv[kMT], mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
       for (int mt = 0; mt < kMT; ++mt) {
-        const int key = tile * kTile + mt * 16, pi = key >> lps & 31;
+        const int key = tile * kTile + mt * 16, pi = (offset_of(cur) + key) >> lps & 31;
         const float k1 = __shfl_sync(0xffffffffu, ks, pi);
         lv[mt] = __shfl_sync(0xffffffffu, lvs, pi);
         f0[mt] = k1 * sf[0];
@@ -884,8 +899,7 @@ cudaError_t launch_decode_t(const CacheGeom& g, const __nv_bfloat16* Q, const ui
 
 }  // namespace
 
-// Keys of a unit, a power of two from 128 on so that the pieces of every unit start on a page: the
-// longest that leaves enough units for each warp, as a unit costs a warp about as much as 40 keys.
+// Keys of a unit, a power of two from 32 (a tile) on: the longest that leaves enough units for each warp, as a unit costs a warp about as much as 40 keys.
 // Units are counted as if half of a group's heads shared their choices.  With more blocks than warps, 3
 // units a warp keep their shares even: 64 caches of 128K take 388 us at 1024 keys, 408 at 256 (32/8 heads
 // of 128, top_k 3 of blocks of 2048); 37 ragged ones of 64 dimensions 57 us at 256, 64 at 512 (blocks of
@@ -893,11 +907,11 @@ cudaError_t launch_decode_t(const CacheGeom& g, const __nv_bfloat16* Q, const ui
 // the memory: eight caches of 128K take 60 us at 1024 keys, 66 at 256; one of 1M 28 us at 128, 38 at 512.
 int cache_chunk_keys(const CacheGeom& g) {
   const int64_t entries = (int64_t)g.B * g.Hkv * ((g.G + 7) / 8);
-  const int64_t past = (g.k - 1) * (1 + (g.G < 8 ? g.G : 8)) / 2, blocks = entries * (1 + (past < g.MB - 1 ? past : g.MB - 1));
+  const int64_t past = (int64_t)(g.k - 1) * (1 + (g.G < 8 ? g.G : 8)) / 2, blocks = entries * (1 + (past < g.MB - 1 ? past : g.MB - 1));
   const int64_t warps = 148 * (g.D == 64 ? AttnLayout<64>::kWarps : AttnLayout<128>::kWarps);
   const int64_t want = blocks >= warps ? 3 * warps : warps * 3 / 5;
   int ck = 8192;
-  while (ck > 128 && (ck / 2 >= g.bs || blocks * ((g.bs + ck - 1) / ck) < want)) ck /= 2;
+  while (ck > 32 && (ck / 2 >= g.bs || blocks * ((g.bs + ck - 1) / ck) < want)) ck /= 2;
   return ck;
 }
 
