@@ -395,6 +395,11 @@ DECODE = [
     (70, 300, 16, 4, 4, 64, 128, 3),          # many short requests
     (2, 5000, 64, 4, 1, 128, 2048, 3),
     (1, 70000, 16, 2, 1, 64, 128, 4),         # 546 candidate blocks, small pages
+    (1, 140000, 128, 1, 1, 64, 128, 3),       # 1093 candidate blocks
+    (800, 20, 16, 2, 2, 128, 128, 2),         # more entries of the work list than are counted one by one
+    (1200, 140, 16, 2, 2, 64, 128, 2),
+    (40, 2100, 64, 8, 8, 64, 1024, 2),        # units of two pieces
+    (30, 1500, 128, 16, 8, 128, 512, 6),      # three units and more for each warp
 ]
 
 
@@ -559,6 +564,45 @@ def test_decode_refuses_other_tensors(cuda_device):
         with pytest.raises(mb.MobaError):
             call(**bad)
     _no_error()
+
+
+def test_decode_far_into_a_large_pool(cuda_device):
+    """Pages whose codes lie behind 4 GB, appended to and read."""
+    import torch
+    mb = _mb()
+    H, ps, D, fmt = 2, 128, 128, "int8"
+    P = 140000  # 4.6 GB of codes each for keys and values
+    p = mb.MobaCacheParams(2, 600, P, ps, 4, H, D, 256, 3, fmt)
+    rng = np.random.default_rng(6)
+    tab = (P - 1 - rng.permutation(10)).reshape(2, 5).astype(np.int32)
+    add, cu = np.array([600, 333], np.int32), np.array([0, 600, 933], np.int32)
+    slots = np.concatenate([tab[s, np.arange(n) // ps] * ps + np.arange(n) % ps for s, n in enumerate(add)]).astype(np.int32)
+    kv, q = _bf16(rng.standard_normal((933, 2, H, D))), _bf16(rng.standard_normal((2, 4, D)))
+    Kc, Vc = (torch.empty(P, H, ps, D, dtype=torch.int8, device="cuda") for _ in range(2))
+    Ks, Vs = (torch.empty(P, H, device="cuda") for _ in range(2))
+    kbar = torch.zeros(2, 3, H, D, device="cuda")
+    mb.moba_cache_append(p, kv[:, 0], kv[:, 1], _dev(cu), _dev(add), _dev(slots), _dev(tab), Kc, Vc, Ks, Vs, kbar)
+    small = type("P", (), {})()  # the ten pages by themselves
+    order = tab.flatten().astype(np.int64)
+    at = torch.from_numpy(order).cuda()
+    kc, vc = (ref.code_values(fmt)[x[at].view(torch.uint8).cpu().numpy()] for x in (Kc, Vc))
+    ks, vs = (x[at].cpu().numpy().astype(np.float64) for x in (Ks, Vs))
+    zero = np.zeros((10, H, ps, D)), np.zeros((10, H))
+    place = np.full(P, -1)
+    place[order] = np.arange(10)
+    near = place[slots // ps] * ps + slots % ps
+    for got, scales, x in ((kc, ks, kv[:, 0]), (vc, vs, kv[:, 1])):
+        want, want_s = ref.append(fmt, ps, 256, x.double().cpu().numpy(), cu, add, near, *zero)
+        used = [place[tab[s, j]] for s, n in enumerate(add) for j in range(-(-n // ps))]
+        np.testing.assert_array_equal(scales[used], want_s[used])
+        for s, n in enumerate(add):
+            for pos in (0, 127, 128, n - 1):
+                np.testing.assert_array_equal(got[place[tab[s, pos // ps]], :, pos % ps], want[place[tab[s, pos // ps]], :, pos % ps])
+    O, LSE, sel = torch.empty_like(q), torch.empty(2, 4, device="cuda"), torch.empty(2, 4, 3, dtype=torch.int32, device="cuda")
+    mb.moba_cache_decode_fwd(p, q, Kc, Vc, Ks, Vs, kbar, _dev(add), _dev(tab), mb.alloc_cache_workspace(p), O, LSE, sel=sel)
+    _no_error()
+    small.values = lambda: (kc, vc, ks, vs)
+    _check_decode(p, small, q, kbar, add, place[tab], (O, LSE, sel))
 
 
 # ---------------------------------------------------------------------------------- together
