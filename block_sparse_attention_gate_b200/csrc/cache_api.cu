@@ -133,13 +133,13 @@ moba_status moba_cache_tables(const moba_cache_params* p, const int32_t* add, co
   if (max_tokens < 0) return fail(MOBA_ERR_INVALID_ARG, "max_tokens must be >= 0 (got %d)", max_tokens);
   MOBA_TRY(check_ptr(add, "add", 4));
   MOBA_TRY(check_ptr(lens, "lens", 4));
-  MOBA_TRY(check_ptr(tables, "tables"));
+  MOBA_TRY(check_ptr(tables, "tables", 4));
   MOBA_TRY(check_ptr(free_pages, "free_pages", 4));
   MOBA_TRY(check_ptr(free_state, "free_state", 4));
   MOBA_TRY(check_ptr(lens_out, "lens_out", 4));
   MOBA_TRY(check_ptr(free_state_out, "free_state_out", 4));
   MOBA_TRY(check_ptr(cu_new, "cu_new", 4));
-  if (max_tokens > 0) MOBA_TRY(check_ptr(slots, "slots"));
+  if (max_tokens > 0) MOBA_TRY(check_ptr(slots, "slots", 4));
   MOBA_TRY(check_ptr(status, "status", 4));
   MOBA_TRY(moba::api::device_error_word(&g.err));
   const cudaError_t e = moba::launch_cache_tables(g, add, lens, tables, free_pages, free_state, lens_out,
@@ -166,8 +166,8 @@ moba_status moba_cache_append(const moba_cache_params* p, const void* K, int64_t
   MOBA_TRY(check_ptr(V, "V"));
   MOBA_TRY(check_ptr(cu_new, "cu_new", 4));
   MOBA_TRY(check_ptr(lens, "lens", 4));
-  MOBA_TRY(check_ptr(slots, "slots"));
-  MOBA_TRY(check_ptr(tables, "tables"));
+  MOBA_TRY(check_ptr(slots, "slots", 4));
+  MOBA_TRY(check_ptr(tables, "tables", 4));
   MOBA_TRY(check_ptr(Kc, "Kc"));
   MOBA_TRY(check_ptr(Vc, "Vc"));
   MOBA_TRY(check_ptr(Ks, "Ks"));
@@ -200,8 +200,8 @@ moba_status moba_cache_decode_fwd(const moba_cache_params* p, const void* Q, con
   MOBA_TRY(check_ptr(Vs, "Vs"));
   MOBA_TRY(check_ptr(Kbar, "Kbar"));
   MOBA_TRY(check_ptr(lens, "lens", 4));
-  MOBA_TRY(check_ptr(tables, "tables"));
-  if (sel) MOBA_TRY(check_ptr(sel, "sel"));
+  MOBA_TRY(check_ptr(tables, "tables", 4));
+  if (sel) MOBA_TRY(check_ptr(sel, "sel", 4));
   MOBA_TRY(check_ptr(O, "O"));
   MOBA_TRY(check_ptr(LSE, "LSE"));
   const size_t need = carve_cache_decode(g, nullptr).bytes;

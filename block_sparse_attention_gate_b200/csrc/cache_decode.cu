@@ -817,15 +817,14 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
 // Codes [P * Hkv, ps, D] as dims (d, row, slab); boxes of D x min(ps, tile) x 1, swizzled over the
 // whole row (128 or 64 bytes).
 cudaError_t make_codes_map(CUtensorMap* m, const void* base, const CacheGeom& g, int tile) {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
+  static const auto fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    if (!fn) return cudaErrorNotSupported;
-  }
+    const bool ok = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+                    q == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
+  }();
+  if (!fn) return cudaErrorNotSupported;
   const cuuint64_t dims[3] = {(cuuint64_t)g.D, (cuuint64_t)g.ps, (cuuint64_t)g.P * g.Hkv};
   const cuuint64_t strides[2] = {(cuuint64_t)g.D, (cuuint64_t)g.D * g.ps};
   const cuuint32_t box[3] = {(cuuint32_t)g.D, (cuuint32_t)(g.ps < tile ? g.ps : tile), 1};

@@ -280,9 +280,13 @@ MOBA_API moba_status moba_fwd_host(const moba_params* p, const void* Q, const vo
  *   Kbar    [max_seqs, ceil(max_seqlen / block_size), Hkv, D] fp32: mean of the stored keys
  *           (code * scale) of each complete MoBA block
  * All of these are DEVICE buffers of the caller; lengths live on the device only, so that a
- * captured CUDA graph of tables -> append -> decode serves step after step.  Int32 vectors need
- * 4-byte alignment, everything else 16.  A captured call uses the buffers it was captured with:
- * two graphs that share a workspace, or a cache, must not run at the same time.
+ * captured CUDA graph of tables -> append -> decode serves step after step (make one call of each
+ * kind before the first capture).  Int32 buffers need 4-byte alignment, everything else 16.  A
+ * captured call uses the buffers it was captured with: two graphs that share a workspace, or a
+ * cache, must not run at the same time.
+ * Scales are positive and finite, as moba_cache_append writes them.  Requests may share pages that
+ * are only read (equal entries of their rows); a page that is written belongs to one request.  A
+ * request only grows or ends: it is not cut back.
  *
  * A page id outside [0, num_pages), a length outside [0, max_seqlen] and a slot that does not
  * fit its token never lead to an access: such tokens are left out (read as masked, not written),
