@@ -353,6 +353,7 @@ class MobaCacheParams:
         self._append = specs("cu_new", "lens", "tables", "Kc", "Vc", "Ks", "Vs", "Kbar")
         self._decode = specs("Q", "Kc", "Vc", "Ks", "Vs", "Kbar", "lens", "tables", "O", "LSE")
         self._sel = specs("sel")
+        self._cuda, self._raw_stream = torch.cuda, getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
     def ref(self):
         return self._ref
@@ -403,14 +404,14 @@ def _on(t):
     return index
 
 
-def _call(index, stream, fn, *args):
+def _call(p, index, stream, fn, *args):
     """fn(*args, stream) with device `index` current, on the given stream or its current one."""
-    import torch
-    cuda = torch.cuda
+    cuda = p._cuda
     if stream is None:
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the address without a Stream object
-        stream = raw(index) if raw is not None else cuda.current_stream(index)
-    stream = getattr(stream, "cuda_stream", stream)
+        # the address alone, where torch gives it without a Stream object
+        stream = p._raw_stream(index) if p._raw_stream is not None else cuda.current_stream(index).cuda_stream
+    else:
+        stream = getattr(stream, "cuda_stream", stream)
     if cuda.current_device() == index:
         rc = fn(*args, stream)
     else:
@@ -427,7 +428,7 @@ def moba_cache_tables(p: MobaCacheParams, add, lens, tables, free_pages, free_st
     index = _on(add)
     ptr = p._pointers(index, p._tables, (add, lens, tables, free_pages, free_state, lens_out, free_state_out, cu_new,
                                          status))
-    _call(index, stream, load().moba_cache_tables, p._ref, *ptr[:8], p._slots(index, slots), slots.shape[0], ptr[8])
+    _call(p, index, stream, load().moba_cache_tables, p._ref, *ptr[:8], p._slots(index, slots), slots.shape[0], ptr[8])
 
 
 def moba_cache_append(p: MobaCacheParams, K, V, cu_new, lens, slots, tables, Kc, Vc, Ks, Vs, Kbar,
@@ -435,21 +436,21 @@ def moba_cache_append(p: MobaCacheParams, K, V, cu_new, lens, slots, tables, Kc,
     """Writes the new tokens K, V [n, Hkv, D] (rows any multiple of 8 elements apart) into their
     slots and pools the keys of blocks that become complete; lens are those after the step."""
     index = _on(K)
-    row, strides = p.c.num_kv_heads * p.c.head_dim, []
-    n = K.shape[0]
-    for name, t in (("K", K), ("V", V)):
-        dtype, shape = p.buffers[name]
-        size, stride = t.shape, t.stride()
-        if (t.dtype is not dtype or len(size) != 3 or size[1:] != shape[1:] or t.get_device() != index
-                or stride[1:] != (size[2], 1)):
-            p._check_one(name, t, index)
-        strides.append(stride[0] if n > 1 else row)
+    dtype, (_, heads, dims) = p.buffers["K"]
+    size, (k_stride, *k_inner), (v_stride, *v_inner) = K.shape, K.stride(), V.stride()
+    n, inner = size[0], [dims, 1]
+    if K.dtype is not dtype or size != (n, heads, dims) or k_inner != inner:
+        p._check_one("K", K, index)
+    if V.dtype is not dtype or V.shape != size or v_inner != inner or V.get_device() != index:
+        p._check_one("V", V, index)
+    if n <= 1:
+        k_stride = v_stride = heads * dims
     ptr = p._pointers(index, p._append, (cu_new, lens, tables, Kc, Vc, Ks, Vs, Kbar))
     slot_ptr = p._slots(index, slots)
     if V.shape[0] != n or slots.shape[0] != n:
         raise MobaError(1, "K, V and slots must have the same number of tokens (got %d, %d, %d)"
                         % (n, V.shape[0], slots.shape[0]))
-    _call(index, stream, load().moba_cache_append, p._ref, K.data_ptr(), strides[0], V.data_ptr(), strides[1], n,
+    _call(p, index, stream, load().moba_cache_append, p._ref, K.data_ptr(), k_stride, V.data_ptr(), v_stride, n,
           ptr[0], ptr[1], slot_ptr, *ptr[2:])
 
 
@@ -466,7 +467,7 @@ def moba_cache_decode_fwd(p: MobaCacheParams, Q, Kc, Vc, Ks, Vs, Kbar, lens, tab
     sel_ptr = p._pointers(index, p._sel, (sel,))[0] if sel is not None else None
     if workspace.get_device() != index or not workspace.is_contiguous():
         raise MobaError(1, "workspace must be contiguous and on %s" % Q.device)
-    _call(index, stream, load().moba_cache_decode_fwd, p._ref, *ptr[:8], sel_ptr, workspace.data_ptr(),
+    _call(p, index, stream, load().moba_cache_decode_fwd, p._ref, *ptr[:8], sel_ptr, workspace.data_ptr(),
           workspace.numel() * workspace.element_size(), *ptr[8:])
 
 

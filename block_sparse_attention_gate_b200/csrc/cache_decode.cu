@@ -32,7 +32,6 @@ constexpr float kLn2C = 0.6931471805599453f;
 
 constexpr int kGateWarps = 8;
 constexpr int kGateRows = 8;   // blocks that a warp scores at a time
-constexpr int kHeld = 16;      // scores that a lane holds while a head's best are picked
 
 // Order of scores as unsigned numbers: NaN last, -0 as +0.  No score maps to 0.
 __device__ __forceinline__ uint64_t score_key(double x) {
@@ -70,6 +69,29 @@ __device__ __forceinline__ int32_t warp_best(uint64_t key, int32_t b) {
   return (int32_t)__reduce_min_sync(0xffffffffu, hi == top && lo == low ? (uint32_t)b : 0xffffffffu);
 }
 
+// The m best of up to 32 * kN keys, each lane holding kN; the q-th goes to lane 1 + q.  A round is a
+// chain of comparisons in the lane and three warp reductions, so it pays to hold no more than needed:
+// 11 rounds over 59 blocks took 3 us of the gate with 16 keys a lane.
+template <int kN>
+__device__ __forceinline__ void pick_best(const uint64_t* keys, int n, int m, int32_t& mine) {
+  const int lane = threadIdx.x & 31;
+  uint64_t held[kN];
+#pragma unroll
+  for (int x = 0; x < kN; ++x) held[x] = x * 32 + lane < n ? keys[x * 32 + lane] : 0;
+  for (int q = 0; q < m; ++q) {
+    uint64_t best = held[0];
+    int at = 0;
+#pragma unroll
+    for (int x = 1; x < kN; ++x)
+      if (held[x] > best) best = held[x], at = x;
+    const int32_t bb = warp_best(best, at * 32 + lane);
+    if (lane == 1 + q) mine = bb;
+#pragma unroll
+    for (int x = 0; x < kN; ++x)
+      if (x * 32 + lane == bb) held[x] = 0;
+  }
+}
+
 // The cluster of a (request, KV head): its CTAs share the earlier blocks' scores (kH heads and 8
 // blocks a warp at a time, a lane per D / 32 dimensions), then CTA 0 chooses, a warp a head, and
 // lists the distinct blocks of every 8 heads.
@@ -84,6 +106,7 @@ __global__ void __launch_bounds__(kGateWarps * 32)
   launch_dependents();  // the attention kernel may be set up meanwhile
   const int32_t len = cached_len(g, lens, s);
   const int i = len > 0 ? (len - 1) / g.bs : -1;
+  const int rows = gridDim.x * kGateWarps * kGateRows;
   const size_t row0 = (size_t)s * g.Hq + (size_t)gk * g.G;
   if (g.k > 1) {
     for (int h0 = 0; h0 < g.G; h0 += kH) {
@@ -93,7 +116,7 @@ __global__ void __launch_bounds__(kGateWarps * 32)
 #pragma unroll
         for (int x = 0; x < kDL; ++x)
           q[h][x] = h0 + h < g.G ? (double)__bfloat162float(Q[(row0 + h0 + h) * kD + lane * kDL + x]) : 0.0;
-      for (int b0 = (rank * kGateWarps + warp) * kGateRows; b0 < i; b0 += gridDim.x * kGateWarps * kGateRows) {
+      for (int b0 = (rank * kGateWarps + warp) * kGateRows; b0 < i; b0 += rows) {
         float kb[kGateRows][kDL];
 #pragma unroll
         for (int r = 0; r < kGateRows; ++r) {
@@ -135,22 +158,15 @@ __global__ void __launch_bounds__(kGateWarps * 32)
     if (hh < g.G) {
       const uint64_t* sc = w.score + (row0 + hh) * g.MB;
       int32_t mine = lane == 0 ? i : -1;  // this lane's entry of the row of sel
-      if (i <= kHeld * 32) {
-        uint64_t held[kHeld];
-#pragma unroll
-        for (int x = 0; x < kHeld; ++x) held[x] = x * 32 + lane < i && m > 0 ? sc[x * 32 + lane] : 0;
-        for (int q = 0; q < m; ++q) {
-          uint64_t best = held[0];
-          int at = 0;
-#pragma unroll
-          for (int x = 1; x < kHeld; ++x)
-            if (held[x] > best) best = held[x], at = x;
-          const int32_t bb = warp_best(best, at * 32 + lane);
-          if (lane == 1 + q) mine = bb;
-#pragma unroll
-          for (int x = 0; x < kHeld; ++x)
-            if (x * 32 + lane == bb) held[x] = 0;
-        }
+      if (m == 0) {
+      } else if (i <= 32) {
+        pick_best<1>(sc, i, m, mine);
+      } else if (i <= 64) {
+        pick_best<2>(sc, i, m, mine);
+      } else if (i <= 128) {
+        pick_best<4>(sc, i, m, mine);
+      } else if (i <= 512) {
+        pick_best<16>(sc, i, m, mine);
       } else {  // too many to hold: each round looks for the best behind the last one
         uint64_t last = ~0ull;
         int32_t last_b = -1;
@@ -739,6 +755,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % kWarps;
   const size_t row = (size_t)blockIdx.x * (kMergeWarps / kWarps) + warp / kWarps;
   const bool live = row < (size_t)g.B * g.Hq;
+  // the gate starts when all earlier work has ended, so the lengths may be read before the wait
   const int32_t len = live ? cached_len(g, lens, (int)(row / g.Hq)) : 0;
   const int own = len > 0 ? (len - 1) / g.bs : 0, own_chunks = (len - own * g.bs + w.CK - 1) / w.CK;
   const int n = own_chunks + min(g.k - 1, own) * w.NC;  // slots are filled from the front
