@@ -309,18 +309,11 @@ struct AppendSide {
   float* scales;
 };
 
-// Page that a request's token at `pos` (packed row t) goes to, -1 if it is left out.
-__device__ __forceinline__ int32_t page_of_slot(const CacheGeom& g, const int32_t* __restrict__ slots, int32_t t, int off) {
-  const int32_t slot = __ldg(slots + t);
+// Page that a token goes to: its slot has to be at the token's offset in a page of the pool; -1 if it
+// is left out.
+__device__ __forceinline__ int32_t page_of_slot(const CacheGeom& g, int32_t slot, int off) {
   if (slot < 0) return -1;
   if (slot % g.ps == off && page_ok(g, slot / g.ps)) return slot / g.ps;
-  if (threadIdx.x == 0) atomicOr(g.err, kErrBadPage);
-  return -1;
-}
-
-__device__ __forceinline__ int32_t page_of_table(const CacheGeom& g, const int32_t* __restrict__ table, int ordinal) {
-  const int32_t page = __ldg(table + ordinal);
-  if (page_ok(g, page)) return page;
   if (threadIdx.x == 0) atomicOr(g.err, kErrBadPage);
   return -1;
 }
@@ -340,7 +333,7 @@ __global__ void __launch_bounds__(kStepThreads)
   int turn = 0;
   for (int32_t pos = start; pos < len;) {
     const int off = pos % g.ps, nr = min(g.ps - off, len - pos);
-    const int32_t t = t0 + (pos - start), page = page_of_slot(g, slots, t, off);
+    const int32_t t = t0 + (pos - start), page = page_of_slot(g, __ldg(slots + t), off);
     if (page >= 0) {
       PageRows<kD, kFmt, 128 * kD / 8 / kStepThreads, kStepThreads> rows;  // any page size
       CodeSums<kFmt, 8> unused;
@@ -442,25 +435,31 @@ __global__ void __launch_bounds__(prompt_threads(kPS), kPS == 128 ? 3 : 6)
     if (nr > 0) Rows::prefetch(ring + stage * kStageBytes, src + (int64_t)t * a.stride, a.stride, nr);
     cp_async_commit();
   };
-  auto slot_page = [&](int p) {
+  // slot of a page's first new token, and the page that the block table names (the pooled key is that of
+  // these pages), read one page ahead and looked at only when it is their turn
+  auto slot_of = [&](int p) -> int32_t {
     int32_t t;
     int nr, off;
     rows_of(p, t, nr, off);
-    return nr > 0 ? page_of_slot(g, slots, t, off) : -1;
+    return nr > 0 ? __ldg(slots + t) : -1;
   };
+  auto listed_at = [&](int p) -> int32_t { return pool && p < p1 ? __ldg(tables + (size_t)s * g.MP + p) : -1; };
 #pragma unroll
   for (int q = 0; q < kAhead; ++q) prefetch(p0 + q, q);
   int turn = 0, stage = 0;
-  int32_t page = slot_page(p0);
+  int32_t slot = slot_of(p0), listed = listed_at(p0);
   float acc[8] = {};
   for (int p = p0; p < p1; ++p) {
     prefetch(p + kAhead, stage == 0 ? kAhead : stage - 1);  // the stage that the last page left
-    const int32_t page_n = slot_page(p + 1);
-    // the pooled key is that of the pages that the block table names
-    const int32_t listed = pool ? page_of_table(g, tables + (size_t)s * g.MP, p) : -1;
+    const int32_t slot_n = slot_of(p + 1), listed_n = listed_at(p + 1);
     int32_t t;
     int nr, off;
     rows_of(p, t, nr, off);
+    const int32_t page = page_of_slot(g, slot, off);
+    if (pool && !page_ok(g, listed)) {
+      if (threadIdx.x == 0) atomicOr(g.err, kErrBadPage);
+      listed = -1;
+    }
     cp_async_wait<kAhead>();
     Rows rows;
     if (page >= 0) rows.take(ring + stage * kStageBytes);
@@ -481,7 +480,8 @@ __global__ void __launch_bounds__(prompt_threads(kPS), kPS == 128 ? 3 : 6)
                                                     a.scales[(size_t)listed * g.Hkv + head], acc);
       }
     }
-    page = page_n;
+    slot = slot_n;
+    listed = listed_n;
     stage = stage == kAhead ? 0 : stage + 1;
   }
   if (!pool) return;  // the same for the whole cluster
