@@ -500,8 +500,8 @@ cudaError_t launch_prompt(const CacheGeom& g, const AppendSide& sk, const Append
                           const int32_t* cu_new, const int32_t* lens, const int32_t* slots, const int32_t* tables,
                           float* Kbar, cudaStream_t st) {
   // CTAs of a cluster: at least 128 rows each, and at most 4 once there are several rounds of CTAs (each
-  // begins with a few loads one behind the other, which longer runs of pages spread): 128K tokens take
-  // 86 us with 4 and 91 with 8, 8K tokens 6.8 with 8 and 8.2 with 4
+  // begins with a few loads one behind the other, which longer runs of pages spread): prompts of 128K
+  // tokens take 77 us with 4, 80 with 8 and 82 with 2; 8K tokens 6.8 with 8 and 8.2 with 4
   const int64_t items = max_tokens / g.bs + 2 * (int64_t)g.B;
   const int most = items * g.Hkv * 2 * 8 > 4 * 148 * 6 ? 4 : 8;
   int ranks = 1;
