@@ -700,6 +700,31 @@ def test_serving_steps(fmt, ps, D, Hq, H, bs, graph, cuda_device):
     _serve(p, fmt, 30, seed=ps, graph=graph)
 
 
+def test_streams_given_by_object_and_by_address(cuda_device):
+    import torch
+    mb = _mb()
+    rng = np.random.default_rng(78)
+    p = mb.MobaCacheParams(2, 900, 30, 64, 4, 2, 64, 128, 3)
+    kv, q = _bf16(rng.standard_normal((1000, 2, 2, 64))), _bf16(rng.standard_normal((2, 4, 64)))
+    add = _dev(np.array([700, 300], np.int32))
+    want = None
+    for how in (None, "object", "address"):
+        c = mb.MobaCache(p)
+        side = torch.cuda.Stream()
+        st = None if how is None else side if how == "object" else side.cuda_stream
+        slots, O, LSE = torch.empty(1000, dtype=torch.int32, device="cuda"), torch.empty_like(q), torch.empty(2, 4, device="cuda")
+        torch.cuda.synchronize()
+        mb.moba_cache_tables(p, add, c.lens, c.tables, c.free_pages, c.free_state, c.lens, c.free_state, c.cu_new, slots,
+                             c.status, stream=st)
+        mb.moba_cache_append(p, kv[:, 0], kv[:, 1], c.cu_new, c.lens, slots, c.tables, c.Kc, c.Vc, c.Ks, c.Vs, c.Kbar,
+                             stream=st)
+        mb.moba_cache_decode_fwd(p, q, c.Kc, c.Vc, c.Ks, c.Vs, c.Kbar, c.lens, c.tables, c.workspace, O, LSE, stream=st)
+        _no_error()
+        assert int(c.status) == 0 and LSE.isfinite().all()
+        want = want or (O, LSE)
+        assert torch.equal(O, want[0]) and torch.equal(LSE, want[1])
+
+
 def test_two_caches_on_two_streams(cuda_device):
     """Independent caches on streams of their own, at the same time."""
     import torch
