@@ -605,6 +605,34 @@ def test_decode_far_into_a_large_pool(cuda_device):
     _check_decode(p, small, q, kbar, add, place[tab], (O, LSE, sel))
 
 
+@pytest.mark.parametrize("B,max_len,Hq,H,D,bs,k", [(2, 3000, 8, 2, 128, 256, 4), (40, 900, 8, 4, 64, 128, 3)])
+def test_decode_calls_back_to_back_share_a_workspace(B, max_len, Hq, H, D, bs, k, cuda_device):
+    """Calls on different inputs, one behind the other without a wait, on one work space."""
+    import torch
+    mb = _mb()
+    rng = np.random.default_rng(B)
+    ps = 32
+    P = B * -(-max_len // ps)
+    p = mb.MobaCacheParams(B, max_len, P, ps, Hq, H, D, bs, k)
+    pool = Pool(rng, B, max_len, P, ps, H, D, "e4m3")
+    kbar, tab = _kbar_of(pool, B, max_len, ps, bs, H, D), _dev(pool.tab)
+    sets = []
+    for _ in range(5):
+        lens = rng.integers(0, max_len + 1, B)
+        q = _bf16(rng.standard_normal((B, Hq, D)))
+        sets.append((q, _dev(lens.astype(np.int32)), _decode(p, pool, q, kbar, lens, pool.tab)))
+    ws, got = mb.alloc_cache_workspace(p), []
+    for i in range(60):
+        q, lens, _ = sets[i % 5]
+        O, LSE = torch.empty_like(q), torch.empty(B, Hq, device="cuda")
+        sel = torch.empty(B, Hq, k, dtype=torch.int32, device="cuda")
+        mb.moba_cache_decode_fwd(p, q, pool.Kc, pool.Vc, pool.Ks, pool.Vs, kbar, lens, tab, ws, O, LSE, sel=sel)
+        got.append((O, LSE, sel))
+    _no_error()
+    for i, g in enumerate(got):
+        assert all((a.view(dtype=t) == b.view(dtype=t)).all() for a, b, t in zip(g, sets[i % 5][2], _int_types()))
+
+
 # ---------------------------------------------------------------------------------- together
 
 class Model:
@@ -698,6 +726,42 @@ def test_serving_steps(fmt, ps, D, Hq, H, bs, graph, cuda_device):
     B, max_len = 6, 700
     p = _mb().MobaCacheParams(B, max_len, B * -(-max_len // ps), ps, Hq, H, D, bs, 3, fmt)
     _serve(p, fmt, 30, seed=ps, graph=graph)
+
+
+def test_graph_replays_without_a_wait_between_them(cuda_device):
+    """A captured step that advances the lengths itself, replayed at once many times: the same as the steps
+    one by one."""
+    import torch
+    mb = _mb()
+    rng = np.random.default_rng(5)
+    p = mb.MobaCacheParams(3, 500, 60, 32, 4, 2, 64, 128, 3, "int8")
+    kv, q = _bf16(rng.standard_normal((200, 2, 2, 64))), _bf16(rng.standard_normal((3, 4, 64)))
+    first, one = _dev(np.array([100, 33, 60], np.int32)), torch.ones(3, dtype=torch.int32, device="cuda")
+    out = []
+    for graph in (False, True):
+        c = mb.MobaCache(p)
+        c.append(kv[:193, 0], kv[:193, 1], c.extend(first, 193))
+
+        def step():
+            slots = c.extend(one, 3)
+            c.append(kv[:3, 0], kv[:3, 1], slots)
+            return c.decode(q)
+
+        O, LSE = step()
+        if graph:
+            G = torch.cuda.CUDAGraph()
+            torch.cuda.synchronize()
+            with torch.cuda.graph(G):
+                O, LSE = step()
+            for _ in range(300):
+                G.replay()
+        else:
+            for _ in range(300):
+                O, LSE = step()
+        _no_error()
+        out.append((O, LSE, c.lens, c.tables, c.free_pages, c.free_state, c.Kc, c.Vc, c.Ks, c.Vs, c.Kbar))
+    assert out[0][2].tolist() == [401, 334, 361]
+    assert all(torch.equal(a, b) for a, b in zip(*out))
 
 
 def test_streams_given_by_object_and_by_address(cuda_device):
