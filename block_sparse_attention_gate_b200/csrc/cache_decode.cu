@@ -478,27 +478,33 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
   };
   const int box = min(g.ps, kTile);
   int wr = 0;  // stage that the next copy goes to
+  auto copy_box = [&](const Piece& p, int32_t page, int key, uint8_t* dst) {
+    const int row = (p.key0 + key) & (g.ps - 1), slab = page * g.Hkv + p.gk;
+    tma_load_3d(dst, &tmK, &full[wr], 0, row, slab);
+    tma_load_3d(dst + L::kHalf, &tmV, &full[wr], 0, row, slab);
+  };
   auto issue = [&](const Piece& p, int32_t page, int tile) {
     uint8_t* dst = ring + wr * 2 * L::kHalf;
-    int32_t pg[kMT];
-#pragma unroll
-    for (int x = 0; x < kMT; ++x) {
-      const int key = tile * kTile + x * box;
-      pg[x] = __shfl_sync(0xffffffffu, page, (offset_of(p) + key) >> lps & 31);
-      if (x * box >= kTile || key >= p.n) pg[x] = -1;
-    }
-    if (lane == 0) {
-      uint32_t boxes = 0;
-#pragma unroll
-      for (int x = 0; x < kMT; ++x) boxes += pg[x] >= 0;
-      if (boxes) mbar_expect_tx(&full[wr], boxes * 2 * box * kD); else mbar_arrive(&full[wr]);
-#pragma unroll
-      for (int x = 0; x < kMT; ++x)
-        if (pg[x] >= 0) {
-          const int row = (p.key0 + tile * kTile + x * box) & (g.ps - 1), slab = pg[x] * g.Hkv + p.gk;
-          tma_load_3d(dst + x * box * kD, &tmK, &full[wr], 0, row, slab);
-          tma_load_3d(dst + L::kHalf + x * box * kD, &tmV, &full[wr], 0, row, slab);
+    const int key = tile * kTile;
+    const int32_t p0 = __shfl_sync(0xffffffffu, page, (offset_of(p) + key) >> lps & 31);
+    if (box == kTile) {  // a tile lies in one page
+      if (lane == 0) {
+        if (p0 >= 0) {
+          mbar_expect_tx(&full[wr], 2 * kTile * kD);
+          copy_box(p, p0, key, dst);
+        } else {
+          mbar_arrive(&full[wr]);
         }
+      }
+    } else {             // pages of 16: two boxes
+      int32_t p1 = __shfl_sync(0xffffffffu, page, (offset_of(p) + key + box) >> lps & 31);
+      if (key + box >= p.n) p1 = -1;
+      if (lane == 0) {
+        const int boxes = (p0 >= 0) + (p1 >= 0);
+        if (boxes) mbar_expect_tx(&full[wr], boxes * 2 * box * kD); else mbar_arrive(&full[wr]);
+        if (p0 >= 0) copy_box(p, p0, key, dst);
+        if (p1 >= 0) copy_box(p, p1, key + box, dst + box * kD);
+      }
     }
     if (++wr == kStages) wr = 0;
   };
