@@ -527,7 +527,8 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
   uint32_t qb[kW][2];
   float sf[2];                  // of heads 2t, 2t + 1: softmax scale over Q's power of two, log2 units
   int q_idx = -1;
-  float o[kW][4], m[2], l[2];
+  float o[kW][4], m[2], l[2];   // m: reference of the weights (below); l: sum of the softmax
+  float base[2], limit[2];      // m, or 0 before the first key; the largest score that m serves
 
   while (true) {
     if (cur.begins) {
@@ -565,8 +566,8 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
       for (int j = 0; j < kW; ++j)
 #pragma unroll
         for (int x = 0; x < 4; ++x) o[j][x] = 0.f;
-      m[0] = m[1] = -INFINITY;
-      l[0] = l[1] = 0.f;
+      m[0] = m[1] = limit[0] = limit[1] = -INFINITY;
+      l[0] = l[1] = base[0] = base[1] = 0.f;
     }
     const float lvs = log2f(vs);
     const int tiles = tiles_of(cur);
@@ -625,10 +626,16 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
 #pragma unroll
       for (int mt = 0; mt < kMT; ++mt) {
         const int key = tile * kTile + mt * 16, pi = (offset_of(cur) + key) >> lps & 31;
-        const float k1 = __shfl_sync(0xffffffffu, ks, pi);
-        lv[mt] = __shfl_sync(0xffffffffu, lvs, pi);
-        f0[mt] = k1 * sf[0];
-        f1[mt] = k1 * sf[1];
+        if (mt > 0 && box == kTile) {  // the same page
+          lv[mt] = lv[0];
+          f0[mt] = f0[0];
+          f1[mt] = f1[0];
+        } else {
+          const float k1 = __shfl_sync(0xffffffffu, ks, pi);
+          lv[mt] = __shfl_sync(0xffffffffu, lvs, pi);
+          f0[mt] = k1 * sf[0];
+          f1[mt] = k1 * sf[1];
+        }
         if constexpr (kOdd) {
           const int32_t pg = __shfl_sync(0xffffffffu, page_c, pi);
           live[mt] = pg >= 0 ? min(16, cur.n - key) : 0;
@@ -648,7 +655,7 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
       // m is a maximum of earlier keys, not the largest so far: weights up to 2^kSlack are as good in fp16
       // and fp32, and the exact maximum over the lanes is only needed when a key leaves that range
       constexpr float kSlack = 8.f;
-      if (__any_sync(0xffffffffu, mx0 > m[0] + kSlack || mx1 > m[1] + kSlack)) {
+      if (__any_sync(0xffffffffu, mx0 > limit[0] || mx1 > limit[1])) {
 #pragma unroll
         for (int off = 4; off <= 16; off <<= 1) {
           mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
@@ -668,8 +675,12 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
         }
         m[0] = mx0;
         m[1] = mx1;
+        base[0] = mx0 == -INFINITY ? 0.f : mx0;
+        base[1] = mx1 == -INFINITY ? 0.f : mx1;
+        limit[0] = mx0 + kSlack;
+        limit[1] = mx1 + kSlack;
       }
-      const float b0 = m[0] == -INFINITY ? 0.f : m[0], b1 = m[1] == -INFINITY ? 0.f : m[1];
+      const float b0 = base[0], b1 = base[1];
       // ---- O += V^T P: dimensions of group gq, heads 2t and 2t + 1
 #pragma unroll
       for (int mt = 0; mt < kMT; ++mt) {
