@@ -355,10 +355,11 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
   wait_for_primary();  // the gate's results
 
   int32_t todo;       // units of this warp that are not opened yet
-  int n_idx, n_unit;  // the next of them
+  int n_idx, n_unit;  // the next of them: entry and number in it,
+  int n_at, n_chunk;  // which is a chunk of the entry's n_at-th block
   int4 n_seg = make_int4(0, 0, 0, 0);
   auto fetch_seg = [&]() {
-    n_seg = __ldcg(reinterpret_cast<const int4*>(w.segs + (size_t)n_idx * w.max_segs + n_unit / w.NC));
+    n_seg = __ldcg(reinterpret_cast<const int4*>(w.segs + (size_t)n_idx * w.max_segs + n_at));
   };
   const int64_t W = (int64_t)gridDim.x * L::kWarps, wid = (int64_t)blockIdx.x * L::kWarps + warp;
   const int per = (NI + L::kMaxPrefix - 1) / L::kMaxPrefix, groups = (NI + per - 1) / per;
@@ -372,6 +373,8 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
     n_idx = u / most;
     n_unit = u - n_idx * most;
     if (n_idx >= NI) return;
+    n_at = n_unit / w.NC;
+    n_chunk = n_unit - n_at * w.NC;
     fetch_seg();
     todo = n_unit < __ldcg(w.units + n_idx);
     if (todo == 0) return;
@@ -416,6 +419,8 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
     n_idx = lo * per;
     n_unit = u - prefix[lo];
     for (int32_t c; n_unit >= (c = units_of(n_idx));) n_unit -= c, ++n_idx;
+    n_at = n_unit / w.NC;
+    n_chunk = n_unit - n_at * w.NC;
     fetch_seg();
   }
 
@@ -440,7 +445,7 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
       o.s = sg / g.Hkv;
       o.gk = sg - o.s * g.Hkv;
     }
-    o.chunk = n_unit % w.NC;
+    o.chunk = n_chunk;
     o.block = n_seg.x;
     o.slots[0] = (uint32_t)n_seg.z;
     o.slots[1] = (uint32_t)n_seg.w;
@@ -450,8 +455,9 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
     o.left = n - o.n;
     o.begins = true;
     ++n_unit;
+    if (++n_chunk == w.NC) n_chunk = 0, ++n_at;
     if (--todo > 0) {
-      while (n_unit >= units_of(n_idx)) n_unit = 0, ++n_idx;
+      while (n_unit >= units_of(n_idx)) n_unit = n_at = n_chunk = 0, ++n_idx;
       fetch_seg();
     }
     return true;
@@ -529,6 +535,7 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
   int q_idx = -1;
   float o[kW][4], m[2], l[2];   // m: reference of the weights (below); l: sum of the softmax
   float base[2], limit[2];      // m, or 0 before the first key; the largest score that m serves
+  bool fresh = true;            // nothing is added up yet
 
   while (true) {
     if (cur.begins) {
@@ -568,6 +575,7 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
         for (int x = 0; x < 4; ++x) o[j][x] = 0.f;
       m[0] = m[1] = limit[0] = limit[1] = -INFINITY;
       l[0] = l[1] = base[0] = base[1] = 0.f;
+      fresh = true;
     }
     const float lvs = log2f(vs);
     const int tiles = tiles_of(cur);
@@ -663,15 +671,17 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
         }
         mx0 = fmaxf(mx0, m[0]);
         mx1 = fmaxf(mx1, m[1]);
-        const float a0 = mx0 == -INFINITY ? 0.f : ex2(m[0] - mx0), a1 = mx1 == -INFINITY ? 0.f : ex2(m[1] - mx1);
-        l[0] *= a0;
-        l[1] *= a1;
+        if (!fresh) {
+          const float a0 = mx0 == -INFINITY ? 0.f : ex2(m[0] - mx0), a1 = mx1 == -INFINITY ? 0.f : ex2(m[1] - mx1);
+          l[0] *= a0;
+          l[1] *= a1;
 #pragma unroll
-        for (int j = 0; j < kW; ++j) {
-          o[j][0] *= a0;
-          o[j][1] *= a1;
-          o[j][2] *= a0;
-          o[j][3] *= a1;
+          for (int j = 0; j < kW; ++j) {
+            o[j][0] *= a0;
+            o[j][1] *= a1;
+            o[j][2] *= a0;
+            o[j][3] *= a1;
+          }
         }
         m[0] = mx0;
         m[1] = mx1;
@@ -680,6 +690,7 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
         limit[0] = mx0 + kSlack;
         limit[1] = mx1 + kSlack;
       }
+      fresh = false;
       const float b0 = base[0], b1 = base[1];
       // ---- O += V^T P: dimensions of group gq, heads 2t and 2t + 1
 #pragma unroll
