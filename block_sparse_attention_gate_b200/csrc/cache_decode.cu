@@ -246,10 +246,10 @@ __global__ void __launch_bounds__(kGateWarps * 32)
 //  - The k index of the products runs through a lane's own bytes, so both operands come out of the
 //    swizzled tiles by 16-byte reads without bank conflicts; only the weights change places between
 //    lanes (movmatrix).
-// Measured (32/8 heads of 128, blocks of 2048, top_k 3, e4m3): 281 MB of eight 128K caches in 52 us (5.4
+// Measured (32/8 heads of 128, blocks of 2048, top_k 3, e4m3): 281 MB of eight 128K caches in 52 us (5.5
 // TB/s, start and tail included), 2.3 GB of 64 of them at 6.2 TB/s, what a copy reaches.  At D 64 the
 // conversions and the softmax of half as many bytes a key bound it: 156 MB of 37 ragged int8 caches in
-// 48 us, issue slots 46 % busy.
+// 45 us, issue slots 48 % busy.
 
 constexpr int kPiece = 256;     // keys whose pages a warp holds at a time (at most 16 pages)
 
@@ -951,8 +951,8 @@ cudaError_t launch_decode_t(const CacheGeom& g, const __nv_bfloat16* Q, const ui
 
 // Keys of a unit, a power of two from 32 (a tile) on: the longest that leaves enough units for each warp, as a unit costs a warp about as much as 40 keys.
 // Units are counted as if half of a group's heads shared their choices.  With more blocks than warps, 3
-// units a warp keep their shares even: 64 caches of 128K take 388 us at 1024 keys, 408 at 256 (32/8 heads
-// of 128, top_k 3 of blocks of 2048); 37 ragged ones of 64 dimensions 57 us at 256, 64 at 512 (blocks of
+// units a warp keep their shares even: 64 caches of 128K take 385 us at 1024 keys, 403 at 256 (32/8 heads
+// of 128, top_k 3 of blocks of 2048); 37 ragged ones of 64 dimensions 51 us at 256, 58 at 512 (blocks of
 // 512).  With fewer, a bit more than half as many units as warps have enough copies on their way to fill
 // the memory: eight caches of 128K take 60 us at 1024 keys, 66 at 256; one of 1M 28 us at 128, 38 at 512.
 int cache_chunk_keys(const CacheGeom& g) {
