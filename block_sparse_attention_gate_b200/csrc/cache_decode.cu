@@ -949,15 +949,17 @@ cudaError_t launch_decode_t(const CacheGeom& g, const __nv_bfloat16* Q, const ui
 
 }  // namespace
 
-// Keys of a unit, a power of two from 32 (a tile) on: the longest that leaves enough units for each warp, as a unit costs a warp about as much as 40 keys.
-// Units are counted as if half of a group's heads shared their choices.  With more blocks than warps, 3
-// units a warp keep their shares even: 64 caches of 128K take 385 us at 1024 keys, 403 at 256 (32/8 heads
-// of 128, top_k 3 of blocks of 2048); 37 ragged ones of 64 dimensions 51 us at 256, 58 at 512 (blocks of
-// 512).  With fewer, a bit more than half as many units as warps have enough copies on their way to fill
-// the memory: eight caches of 128K take 60 us at 1024 keys, 66 at 256; one of 1M 28 us at 128, 38 at 512.
+// Keys of a unit, a power of two from 32 (a tile) on: the longest that leaves enough units for each warp,
+// as a unit costs a warp about as much as 40 keys.  Units are counted as if half of a group's heads shared
+// their choices.  With more blocks than warps, 3 units a warp keep their shares even: 64 caches of 128K
+// take 385 us at 1024 keys, 403 at 256 (32/8 heads of 128, top_k 3 of blocks of 2048); 37 ragged ones of
+// 64 dimensions 51 us at 256, 58 at 512 (blocks of 512).  With fewer, a bit more than half as many units
+// as warps have enough copies on their way to fill the memory: eight caches of 128K take 57 us at 1024
+// keys, 64 at 256; one of 1M 21 us at 256, 22 at 128, 28 at 512.
 int cache_chunk_keys(const CacheGeom& g) {
   const int64_t entries = (int64_t)g.B * g.Hkv * ((g.G + 7) / 8);
-  const int64_t past = (int64_t)(g.k - 1) * (1 + (g.G < 8 ? g.G : 8)) / 2, blocks = entries * (1 + (past < g.MB - 1 ? past : g.MB - 1));
+  const int64_t past = (int64_t)(g.k - 1) * (1 + (g.G < 8 ? g.G : 8)) / 2;
+  const int64_t blocks = entries * (1 + (past < g.MB - 1 ? past : g.MB - 1));
   const int64_t warps = 148 * (g.D == 64 ? AttnLayout<64>::kWarps : AttnLayout<128>::kWarps);
   const int64_t want = blocks >= warps ? 3 * warps : warps * 3 / 5;
   int ck = 8192;
