@@ -16,9 +16,9 @@
 //   cache_append_kernel : a CTA for each (request, KV head, K or V) takes the request's touched
 //                         pages one after the other: one launch of few CTAs for decode steps (2.7 us
 //                         for 8 requests, 5.8 us for 64 of which some complete a block of 512).
-//   cache_prompt_kernel : a cluster of up to 8 CTAs for each (touched MoBA block, KV head, K or V);
+//   cache_prompt_kernel : a cluster of up to 8 CTAs for each (touched MoBA block, KV head, K or half of V);
 //                         its CTAs share the block's pages and add up the pooled key on the way
-//                         (54769 tokens, 8 heads of 128, pages of 64: 336 MB in 65 us, 5.2 TB/s).
+//                         (54769 tokens, 8 heads of 128, pages of 64: 336 MB in 63 us, 5.4 TB/s).
 #include <float.h>
 
 #include "cache.cuh"
@@ -420,7 +420,11 @@ __global__ void __launch_bounds__(prompt_threads(kPS), kPS == 128 ? 3 : 6)
   if (n <= 0 || start < 0 || b < 0 || (int64_t)b * g.bs >= len) return;  // the same for the whole cluster
   const bool pool = !is_v && (int64_t)(b + 1) * g.bs <= len;
   const int R = g.bs / g.ps, per = (R + ranks - 1) / ranks;
-  const int p0 = b * R + rank * per, p1 = b * R + min(R, (rank + 1) * per);
+  int p0 = b * R + rank * per, p1 = b * R + min(R, (rank + 1) * per);
+  if (is_v) {  // in halves: the short CTAs come last and fill the last round of CTAs (3 % of a long prompt)
+    const int half = (max(p1 - p0, 0) + 1) / 2;
+    if (blockIdx.z == 1) p1 = min(p1, p0 + half); else p0 += half;
+  }
   const __nv_bfloat16* src = a.src + (size_t)head * kD;
   // new rows of page ordinal p: packed row of the first, how many, and the older rows before them
   auto rows_of = [&](int p, int32_t& t, int& nr, int& off) {
@@ -503,13 +507,13 @@ cudaError_t launch_prompt(const CacheGeom& g, const AppendSide& sk, const Append
                           float* Kbar, cudaStream_t st) {
   // CTAs of a cluster: at least 128 rows each, and at most 4 once there are several rounds of CTAs (each
   // begins with a few loads one behind the other, which longer runs of pages spread): prompts of 128K
-  // tokens take 77 us with 4, 80 with 8 and 82 with 2; 8K tokens 6.8 with 8 and 8.2 with 4
+  // tokens took 77 us with 4, 80 with 8 and 82 with 2; 8K tokens 6.8 with 8 and 8.2 with 4
   const int64_t items = max_tokens / g.bs + 2 * (int64_t)g.B;
   const int most = items * g.Hkv * 2 * 8 > 4 * 148 * 6 ? 4 : 8;
   int ranks = 1;
   while (ranks < most && 2 * ranks * 128 <= g.bs) ranks *= 2;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(items * ranks), (unsigned)g.Hkv, 2);
+  cfg.gridDim = dim3((unsigned)(items * ranks), (unsigned)g.Hkv, 3);
   cfg.blockDim = dim3(prompt_threads(kPS));
   cfg.dynamicSmemBytes = (kAhead + 1) * kPS * kD * 2;
   cfg.stream = st;
