@@ -333,7 +333,8 @@ template <int kD, int kFmt>
 __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, CacheGeom g,
                       const __nv_bfloat16* __restrict__ Q, const float* __restrict__ Ks, const float* __restrict__ Vs,
-                      const int32_t* __restrict__ lens, const int32_t* __restrict__ tables, CacheDecodeWork w, int NI) {
+                      const int32_t* __restrict__ lens, const int32_t* __restrict__ tables, CacheDecodeWork w, int NI,
+                      bool own_only) {
   using L = AttnLayout<kD>;
   constexpr int kStages = L::kStages, kTile = L::kTile, kMT = kTile / 16;
   constexpr int kW = kD / 16;   // k steps of K Q^T = 16-row tiles of V^T
@@ -352,18 +353,31 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
     prefetch_tmap(&tmV);
   }
   launch_dependents();
-  wait_for_primary();  // the gate's results
+  wait_for_primary();  // the gate's results (at once where there is none)
 
   int32_t todo;       // units of this warp that are not opened yet
   int n_idx, n_unit;  // the next of them: entry and number in it,
   int n_at, n_chunk;  // which is a chunk of the entry's n_at-th block
   int4 n_seg = make_int4(0, 0, 0, 0);
+  // Where no request can have an earlier block to choose, there is no gate (own_only): an entry's only
+  // block follows from the length.
+  const int HT = (g.G + 7) / 8;
+  auto length_of = [&](int idx) { return cached_len(g, lens, idx / (HT * g.Hkv)); };
+  auto own_keys = [&](int32_t len) { return len > 0 ? len - (len - 1) / g.bs * g.bs : 0; };
+  auto units_in = [&](int idx) { return own_only ? (own_keys(length_of(idx)) + w.CK - 1) / w.CK : __ldcg(w.units + idx); };
   auto fetch_seg = [&]() {
-    n_seg = __ldcg(reinterpret_cast<const int4*>(w.segs + (size_t)n_idx * w.max_segs + n_at));
+    if (own_only) {
+      const int32_t len = length_of(n_idx);
+      const int heads = min(8, g.G - n_idx % HT * 8);
+      n_seg = make_int4((len - 1) / g.bs, own_keys(len), heads >= 4 ? 0 : (int)(~0u << 8 * heads),
+                        heads >= 8 ? 0 : heads <= 4 ? -1 : (int)(~0u << 8 * (heads - 4)));
+    } else {
+      n_seg = __ldcg(reinterpret_cast<const int4*>(w.segs + (size_t)n_idx * w.max_segs + n_at));
+    }
   };
   const int64_t W = (int64_t)gridDim.x * L::kWarps, wid = (int64_t)blockIdx.x * L::kWarps + warp;
   const int per = (NI + L::kMaxPrefix - 1) / L::kMaxPrefix, groups = (NI + per - 1) / per;
-  auto units_of = [&](int idx) { return per == 1 ? prefix[idx + 1] - prefix[idx] : __ldcg(w.units + idx); };
+  auto units_of = [&](int idx) { return per == 1 ? prefix[idx + 1] - prefix[idx] : units_in(idx); };
   // ---- which units: where there is a warp for every one that an entry can have, each warp (spread over
   // the SMs) looks at its own; else the warps take equal runs of those that there are
   const int most = w.max_segs * w.NC;
@@ -376,7 +390,7 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
     n_at = n_unit / w.NC;
     n_chunk = n_unit - n_at * w.NC;
     fetch_seg();
-    todo = n_unit < __ldcg(w.units + n_idx);
+    todo = n_unit < units_in(n_idx);
     if (todo == 0) return;
   } else {
     // units before each group of `per` entries
@@ -387,7 +401,7 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
       const int gr = threadIdx.x * kEach + x;
       cnt[x] = 0;
       if (gr < groups)
-        for (int y = gr * per; y < min(NI, (gr + 1) * per); ++y) cnt[x] += __ldcg(w.units + y);
+        for (int y = gr * per; y < min(NI, (gr + 1) * per); ++y) cnt[x] += units_in(y);
       sum += cnt[x];
     }
     int32_t inc = sum;
@@ -440,7 +454,7 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
     o.idx = n_idx;
     o.s = p.s, o.gk = p.gk, o.ht = p.ht;
     if (n_idx != p.idx) {
-      const int HT = (g.G + 7) / 8, sg = n_idx / HT;
+      const int sg = n_idx / HT;
       o.ht = n_idx - sg * HT;
       o.s = sg / g.Hkv;
       o.gk = sg - o.s * g.Hkv;
@@ -782,14 +796,14 @@ constexpr int kMergeRows = 8;   // partial rows of a warp on their way at a time
 
 template <int kD, int kWarps>
 __global__ void __launch_bounds__(kMergeWarps * 32)
-    cache_merge_kernel(CacheGeom g, const int32_t* __restrict__ lens, CacheDecodeWork w, __nv_bfloat16* __restrict__ O,
-                       float* __restrict__ LSE) {
+    cache_merge_kernel(CacheGeom g, const int32_t* __restrict__ lens, CacheDecodeWork w, bool own_only,
+                       int32_t* __restrict__ sel, __nv_bfloat16* __restrict__ O, float* __restrict__ LSE) {
   constexpr int kDL = kD / 32;
   __shared__ float s_acc[kMergeWarps][kD], s_l[kMergeWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % kWarps;
   const size_t row = (size_t)blockIdx.x * (kMergeWarps / kWarps) + warp / kWarps;
   const bool live = row < (size_t)g.B * g.Hq;
-  // the gate starts when all earlier work has ended, so the lengths may be read before the wait
+  // the step's first kernel starts when all earlier work has ended, so the lengths may be read before the wait
   const int32_t len = live ? cached_len(g, lens, (int)(row / g.Hq)) : 0;
   const int own = len > 0 ? (len - 1) / g.bs : 0, own_chunks = (len - own * g.bs + w.CK - 1) / w.CK;
   const int n = own_chunks + min(g.k - 1, own) * w.NC;  // slots are filled from the front
@@ -861,6 +875,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   for (int d = 0; d < kDL; d += 2)
     *reinterpret_cast<__nv_bfloat162*>(O + row * kD + lane * kDL + d) = __floats2bfloat162_rn(acc[d] * inv, acc[d + 1] * inv);
   if (lane == 0) LSE[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2C;
+  if (own_only && lane < g.k) sel[row * g.k + lane] = lane == 0 && len > 0 ? own : -1;  // there was no gate
 }
 
 // ---------------------------------------------------------------------------------- launch
@@ -906,9 +921,11 @@ cudaError_t launch_gate(const CacheGeom& g, const __nv_bfloat16* Q, const float*
   return cudaLaunchKernelEx(&cfg, cache_gate_kernel<kD, kH>, g, Q, Kbar, lens, sel, w);
 }
 
-// A kernel whose CTAs may start while the one before it runs, and wait for its results there.
+// Launches a kernel; a dependent one's CTAs may start while the kernel before it runs, and wait for its
+// results there.
 template <typename... P, typename... A>
-cudaError_t launch_dependent(dim3 grid, int threads, size_t smem, cudaStream_t st, void (*kernel)(P...), A&&... args) {
+cudaError_t launch_kernel(bool dependent, dim3 grid, int threads, size_t smem, cudaStream_t st, void (*kernel)(P...),
+                          A&&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
@@ -918,7 +935,7 @@ cudaError_t launch_dependent(dim3 grid, int threads, size_t smem, cudaStream_t s
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = dependent ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
@@ -927,7 +944,9 @@ cudaError_t launch_decode_t(const CacheGeom& g, const __nv_bfloat16* Q, const ui
                             const float* Ks, const float* Vs, const float* Kbar, const int32_t* lens,
                             const int32_t* tables, int32_t* sel, const CacheDecodeWork& w, __nv_bfloat16* O,
                             float* LSE, int sms, cudaStream_t st) {
-  cudaError_t e = g.G == 1   ? launch_gate<kD, 1>(g, Q, Kbar, lens, sel, w, st)
+  const bool own_only = g.MB == 1 || g.k == 1;
+  cudaError_t e = own_only   ? cudaSuccess
+                  : g.G == 1 ? launch_gate<kD, 1>(g, Q, Kbar, lens, sel, w, st)
                   : g.G == 2 ? launch_gate<kD, 2>(g, Q, Kbar, lens, sel, w, st)
                              : launch_gate<kD, 4>(g, Q, Kbar, lens, sel, w, st);
   if (e != cudaSuccess) return e;
@@ -935,16 +954,17 @@ cudaError_t launch_decode_t(const CacheGeom& g, const __nv_bfloat16* Q, const ui
   if ((e = make_codes_map(&tk, Kc, g, AttnLayout<kD>::kTile)) != cudaSuccess) return e;
   if ((e = make_codes_map(&tv, Vc, g, AttnLayout<kD>::kTile)) != cudaSuccess) return e;
   if ((e = allow_smem<cache_attn_kernel<kD, kFmt>>(AttnLayout<kD>::kAlloc)) != cudaSuccess) return e;
-  e = launch_dependent(dim3((unsigned)sms), AttnLayout<kD>::kWarps * 32, AttnLayout<kD>::kAlloc, st, cache_attn_kernel<kD, kFmt>, tk, tv, g, Q, Ks, Vs,
-                       lens, tables, w, g.B * g.Hkv * ((g.G + 7) / 8));
+  e = launch_kernel(!own_only, dim3((unsigned)sms), AttnLayout<kD>::kWarps * 32, AttnLayout<kD>::kAlloc, st,
+                    cache_attn_kernel<kD, kFmt>, tk, tv, g, Q, Ks, Vs, lens, tables, w, g.B * g.Hkv * ((g.G + 7) / 8),
+                    own_only);
   if (e != cudaSuccess) return e;
   // many parts: all warps of a CTA on one row (a warp has eight rows on their way at a time)
   const int64_t rows = (int64_t)g.B * g.Hq;
   if (g.k * w.NC > 8)
-    return launch_dependent(dim3((unsigned)rows), kMergeWarps * 32, 0, st, cache_merge_kernel<kD, kMergeWarps>, g, lens, w,
-                            O, LSE);
-  return launch_dependent(dim3((unsigned)((rows + kMergeWarps - 1) / kMergeWarps)), kMergeWarps * 32, 0, st,
-                          cache_merge_kernel<kD, 1>, g, lens, w, O, LSE);
+    return launch_kernel(true, dim3((unsigned)rows), kMergeWarps * 32, 0, st, cache_merge_kernel<kD, kMergeWarps>, g, lens,
+                         w, own_only, sel, O, LSE);
+  return launch_kernel(true, dim3((unsigned)((rows + kMergeWarps - 1) / kMergeWarps)), kMergeWarps * 32, 0, st,
+                       cache_merge_kernel<kD, 1>, g, lens, w, own_only, sel, O, LSE);
 }
 
 }  // namespace

@@ -396,6 +396,10 @@ DECODE = [
     (2, 5000, 64, 4, 1, 128, 2048, 3),
     (1, 70000, 16, 2, 1, 64, 128, 4),         # 546 candidate blocks, small pages
     (1, 140000, 128, 1, 1, 64, 128, 3),       # 1093 candidate blocks
+    (5, 127, 16, 6, 2, 64, 128, 4),           # requests of one block at most: nothing to choose from
+    (7, 2000, 64, 36, 2, 128, 2048, 3),       # the same, 18 heads to a group
+    (3, 1000, 32, 10, 2, 128, 256, 1),        # top_k 1: the own block alone
+    (900, 130, 32, 4, 2, 128, 256, 3),        # the same with a long work list
     (800, 20, 16, 2, 2, 128, 128, 2),         # more entries of the work list than are counted one by one
     (1200, 140, 16, 2, 2, 64, 128, 2),
     (40, 2100, 64, 8, 8, 64, 1024, 2),        # units of two pieces
