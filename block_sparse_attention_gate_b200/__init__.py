@@ -352,7 +352,7 @@ class MobaCacheParams:
                              "status")
         self._append = specs("cu_new", "lens", "tables", "Kc", "Vc", "Ks", "Vs", "Kbar")
         self._decode = specs("Q", "Kc", "Vc", "Ks", "Vs", "Kbar", "lens", "tables", "O", "LSE")
-        self._sel = specs("sel")
+        self._decode_sel = self._decode + specs("sel")
         self._cuda, self._raw_stream = torch.cuda, getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
     def ref(self):
@@ -463,12 +463,14 @@ def moba_cache_decode_fwd(p: MobaCacheParams, Q, Kc, Vc, Ks, Vs, Kbar, lens, tab
     """Gated decode: Q [max_seqs, Hq, D] (the newest token of each request) against the paged 8-bit
     cache; O [max_seqs, Hq, D], LSE [max_seqs, Hq], and sel [max_seqs, Hq, top_k] if given."""
     index = _on(Q)
-    ptr = p._pointers(index, p._decode, (Q, Kc, Vc, Ks, Vs, Kbar, lens, tables, O, LSE))
-    sel_ptr = p._pointers(index, p._sel, (sel,))[0] if sel is not None else None
+    if sel is None:
+        ptr = p._pointers(index, p._decode, (Q, Kc, Vc, Ks, Vs, Kbar, lens, tables, O, LSE)) + [None]
+    else:
+        ptr = p._pointers(index, p._decode_sel, (Q, Kc, Vc, Ks, Vs, Kbar, lens, tables, O, LSE, sel))
     if workspace.get_device() != index or not workspace.is_contiguous():
         raise MobaError(1, "workspace must be contiguous and on %s" % Q.device)
-    _call(p, index, stream, load().moba_cache_decode_fwd, p._ref, *ptr[:8], sel_ptr, workspace.data_ptr(),
-          workspace.numel() * workspace.element_size(), *ptr[8:])
+    _call(p, index, stream, load().moba_cache_decode_fwd, p._ref, *ptr[:8], ptr[10], workspace.data_ptr(), workspace.nbytes,
+          ptr[8], ptr[9])
 
 
 def alloc_cache_workspace(p: MobaCacheParams, device="cuda"):

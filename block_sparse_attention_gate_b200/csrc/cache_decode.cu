@@ -880,26 +880,31 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
 
 // ---------------------------------------------------------------------------------- launch
 
+// A driver entry point, looked up once.
+template <typename F>
+F driver_entry(const char* name) {
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  const bool ok = cudaGetDriverEntryPoint(name, &p, cudaEnableDefault, &q) == cudaSuccess && q == cudaDriverEntryPointSuccess;
+  return ok ? reinterpret_cast<F>(p) : nullptr;
+}
+
 // Codes [P * Hkv, ps, D] as dims (d, row, slab); boxes of D x min(ps, tile) x 1, swizzled over the
-// whole row (128 or 64 bytes).
-cudaError_t make_codes_map(CUtensorMap* m, const void* base, const CacheGeom& g, int tile) {
-  static const auto fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    const bool ok = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-                    q == cudaDriverEntryPointSuccess;
-    return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
-  }();
-  if (!fn) return cudaErrorNotSupported;
+// whole row (128 or 64 bytes).  The two maps differ in their address alone.
+cudaError_t make_codes_maps(CUtensorMap* k, CUtensorMap* v, const void* Kc, const void* Vc, const CacheGeom& g, int tile) {
+  static const auto encode = driver_entry<PFN_cuTensorMapEncodeTiled_v12000>("cuTensorMapEncodeTiled");
+  static const auto replace = driver_entry<PFN_cuTensorMapReplaceAddress_v12000>("cuTensorMapReplaceAddress");
+  if (!encode || !replace) return cudaErrorNotSupported;
   const cuuint64_t dims[3] = {(cuuint64_t)g.D, (cuuint64_t)g.ps, (cuuint64_t)g.P * g.Hkv};
   const cuuint64_t strides[2] = {(cuuint64_t)g.D, (cuuint64_t)g.D * g.ps};
   const cuuint32_t box[3] = {(cuuint32_t)g.D, (cuuint32_t)(g.ps < tile ? g.ps : tile), 1};
   const cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        g.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  if (encode(k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(Kc), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, g.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  *v = *k;
+  return replace(v, const_cast<void*>(Vc)) == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 template <int kD, int kH>
@@ -951,8 +956,7 @@ cudaError_t launch_decode_t(const CacheGeom& g, const __nv_bfloat16* Q, const ui
                              : launch_gate<kD, 4>(g, Q, Kbar, lens, sel, w, st);
   if (e != cudaSuccess) return e;
   CUtensorMap tk, tv;
-  if ((e = make_codes_map(&tk, Kc, g, AttnLayout<kD>::kTile)) != cudaSuccess) return e;
-  if ((e = make_codes_map(&tv, Vc, g, AttnLayout<kD>::kTile)) != cudaSuccess) return e;
+  if ((e = make_codes_maps(&tk, &tv, Kc, Vc, g, AttnLayout<kD>::kTile)) != cudaSuccess) return e;
   if ((e = allow_smem<cache_attn_kernel<kD, kFmt>>(AttnLayout<kD>::kAlloc)) != cudaSuccess) return e;
   e = launch_kernel(!own_only, dim3((unsigned)sms), AttnLayout<kD>::kWarps * 32, AttnLayout<kD>::kAlloc, st,
                     cache_attn_kernel<kD, kFmt>, tk, tv, g, Q, Ks, Vs, lens, tables, w, g.B * g.Hkv * ((g.G + 7) / 8),
