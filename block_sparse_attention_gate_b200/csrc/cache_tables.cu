@@ -160,9 +160,9 @@ __global__ void __launch_bounds__(kTabThreads)
       const int j = owner_of(s_back, live, i);
       free_pages[ring(end + (uint32_t)(base.back + i))] = tables[(int64_t)(b0 + j) * g.MP + (i - s_back[j])];
     }
-    for (int32_t i = first; i < (int32_t)t.n; i += step) {
-      const int j = owner_of(s_tok, live, i);
-      const int32_t pos = s_len[j] + (i - s_tok[j]), nth = (pos >> lps) - ((s_len[j] + g.ps - 1) >> lps);
+    for (int64_t i = first; i < t.n; i += step) {
+      const int j = owner_of(s_tok, live, (int32_t)i);
+      const int32_t pos = s_len[j] + ((int32_t)i - s_tok[j]), nth = (pos >> lps) - ((s_len[j] + g.ps - 1) >> lps);
       // a new page is read where the entry above comes from
       const int32_t page = nth < 0 ? tables[(int64_t)(b0 + j) * g.MP + (pos >> lps)] : taken(s_need[j] + nth);
       slots[base.n + i] = page_ok(g, page) ? (page << lps) + (pos & (g.ps - 1)) : -1;
