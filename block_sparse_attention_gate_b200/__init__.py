@@ -322,9 +322,9 @@ class MobaCacheParams:
                                block_size, top_k, CACHE_FORMATS[format], softmax_scale)
         self._ref = ctypes.byref(self.c)
         self.format = format
-        self.workspace_bytes = int(load().moba_cache_decode_workspace_size(self.ref()))
-        if not self.workspace_bytes:
-            raise MobaError(2, load().moba_last_error().decode())
+        # an append of no tokens checks the parameters and does nothing else
+        _check(load().moba_cache_append(self._ref, None, 0, None, 0, 0, *[None] * 9, None))
+        self.workspace_bytes = int(load().moba_cache_decode_workspace_size(self._ref))
         self.pages_per_seq = -(-max_seqlen // page_size)
         self.max_blocks = -(-max_seqlen // block_size)
         import torch

@@ -230,8 +230,8 @@ __global__ void __launch_bounds__(kGateWarps * 32)
 
 // ------------------------------------------------------------------------------- attention
 //
-// Every warp works alone: it has a ring of kStages tiles of 32 keys (keys and values, by TMA) and
-// takes a contiguous run of the units (chunks of CK keys of a distinct block).  One query for each
+// Every warp works alone: it has a ring of kStages tiles of 32 keys (keys and values, by TMA) and its
+// share of the units (chunks of CK keys of a distinct block).  One query for each
 // of up to 8 heads: S = K Q^T and O += V^T P on mma.m16n8k16, with keys (dimensions) as the 16
 // rows and the heads as the 8 columns, so that the codes, converted in registers to fp16 (exact),
 // are the large operand and nothing is padded.  tcgen05 has nothing to win here: its operands would

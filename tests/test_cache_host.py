@@ -20,8 +20,9 @@ GOOD = dict(max_seqs=3, max_seqlen=1000, num_pages=50, page_size=32, num_q_heads
     (dict(top_k=0), 2), (dict(top_k=17), 2), (dict(max_seqlen=1 << 22, block_size=128), 2),
     (dict(max_seqs=65535, max_seqlen=1 << 20, page_size=16), 2)])
 def test_bad_params_are_refused(change, status):
-    with pytest.raises(mb.MobaError):
+    with pytest.raises(mb.MobaError) as e:
         mb.MobaCacheParams(**{**GOOD, **change})
+    assert e.value.status == status
     p = mb.MobaCacheParams(**GOOD)
     for name, value in change.items():
         setattr(p.c, name, value)
