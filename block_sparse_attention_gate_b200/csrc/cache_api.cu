@@ -109,7 +109,7 @@ moba::CacheDecodeWork carve_cache_decode(const moba::CacheGeom& g, char* base) {
   w.max_segs = cache_max_segs(g);
   const size_t rows = (size_t)g.B * g.Hq, parts = rows * g.k * w.NC;
   const size_t entries = (size_t)g.B * g.Hkv * ((g.G + 7) / 8);
-  w.score = (uint64_t*)take(g.k > 1 ? rows * g.MB * sizeof(uint64_t) : 0);
+  w.score = (uint64_t*)take(rows * g.MB * sizeof(uint64_t));
   w.segs = (moba::CacheSeg*)take(entries * w.max_segs * sizeof(moba::CacheSeg));
   w.units = (int32_t*)take(entries * sizeof(int32_t));
   w.part_o = (float*)take(parts * g.D * sizeof(float));

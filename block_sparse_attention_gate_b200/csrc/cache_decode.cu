@@ -110,49 +110,47 @@ __global__ void __launch_bounds__(kGateWarps * 32)
   const int i = len > 0 ? (len - 1) / g.bs : -1;
   const int rows = gridDim.x * kGateWarps * kGateRows;
   const size_t row0 = (size_t)s * g.Hq + (size_t)gk * g.G;
-  if (g.k > 1) {
-    for (int h0 = 0; h0 < g.G; h0 += kH) {
-      double q[kH][kDL];
+  for (int h0 = 0; h0 < g.G; h0 += kH) {
+    double q[kH][kDL];
 #pragma unroll
-      for (int h = 0; h < kH; ++h)
+    for (int h = 0; h < kH; ++h)
 #pragma unroll
-        for (int x = 0; x < kDL; ++x)
-          q[h][x] = h0 + h < g.G ? (double)__bfloat162float(Q[(row0 + h0 + h) * kD + lane * kDL + x]) : 0.0;
-      for (int b0 = (rank * kGateWarps + warp) * kGateRows; b0 < i; b0 += rows) {
-        float kb[kGateRows][kDL];
+      for (int x = 0; x < kDL; ++x)
+        q[h][x] = h0 + h < g.G ? (double)__bfloat162float(Q[(row0 + h0 + h) * kD + lane * kDL + x]) : 0.0;
+    for (int b0 = (rank * kGateWarps + warp) * kGateRows; b0 < i; b0 += rows) {
+      float kb[kGateRows][kDL];
 #pragma unroll
-        for (int r = 0; r < kGateRows; ++r) {
-          const float* src = Kbar + (((size_t)s * g.MB + b0 + r) * g.Hkv + gk) * kD + lane * kDL;
-          if (b0 + r < i) {
-            if constexpr (kDL == 4) {
-              const float4 f = __ldg(reinterpret_cast<const float4*>(src));
-              kb[r][0] = f.x, kb[r][1] = f.y, kb[r][2] = f.z, kb[r][3] = f.w;
-            } else {
-              const float2 f = __ldg(reinterpret_cast<const float2*>(src));
-              kb[r][0] = f.x, kb[r][1] = f.y;
-            }
+      for (int r = 0; r < kGateRows; ++r) {
+        const float* src = Kbar + (((size_t)s * g.MB + b0 + r) * g.Hkv + gk) * kD + lane * kDL;
+        if (b0 + r < i) {
+          if constexpr (kDL == 4) {
+            const float4 f = __ldg(reinterpret_cast<const float4*>(src));
+            kb[r][0] = f.x, kb[r][1] = f.y, kb[r][2] = f.z, kb[r][3] = f.w;
           } else {
-#pragma unroll
-            for (int x = 0; x < kDL; ++x) kb[r][x] = 0.f;
+            const float2 f = __ldg(reinterpret_cast<const float2*>(src));
+            kb[r][0] = f.x, kb[r][1] = f.y;
           }
+        } else {
+#pragma unroll
+          for (int x = 0; x < kDL; ++x) kb[r][x] = 0.f;
         }
-        double v[kGateRows * kH];
-#pragma unroll
-        for (int r = 0; r < kGateRows; ++r)
-#pragma unroll
-          for (int h = 0; h < kH; ++h) {
-            double acc = 0.0;
-#pragma unroll
-            for (int x = 0; x < kDL; ++x) acc = fma(q[h][x], (double)kb[r][x], acc);
-            v[r * kH + h] = acc;
-          }
-        const uint64_t key = score_key(warp_sums<kGateRows * kH>(v));
-        const int x = lane / (4 / kH), r = x / kH, h = x % kH;
-        if (lane % (4 / kH) == 0 && b0 + r < i && h0 + h < g.G) w.score[(row0 + h0 + h) * g.MB + b0 + r] = key;
       }
+      double v[kGateRows * kH];
+#pragma unroll
+      for (int r = 0; r < kGateRows; ++r)
+#pragma unroll
+        for (int h = 0; h < kH; ++h) {
+          double acc = 0.0;
+#pragma unroll
+          for (int x = 0; x < kDL; ++x) acc = fma(q[h][x], (double)kb[r][x], acc);
+          v[r * kH + h] = acc;
+        }
+      const uint64_t key = score_key(warp_sums<kGateRows * kH>(v));
+      const int x = lane / (4 / kH), r = x / kH, h = x % kH;
+      if (lane % (4 / kH) == 0 && b0 + r < i && h0 + h < g.G) w.score[(row0 + h0 + h) * g.MB + b0 + r] = key;
     }
-    if (gridDim.x > 1) cluster_barrier(); else __syncthreads();
   }
+  if (gridDim.x > 1) cluster_barrier(); else __syncthreads();
   if (rank != 0) return;
   const int m = min(g.k - 1, max(i, 0)), HT = (g.G + 7) / 8;
   for (int ht = 0; ht < HT; ++ht) {
@@ -231,18 +229,17 @@ __global__ void __launch_bounds__(kGateWarps * 32)
 // ------------------------------------------------------------------------------- attention
 //
 // Every warp works alone: it has a ring of kStages tiles of 32 keys (keys and values, by TMA) and its
-// share of the units (chunks of CK keys of a distinct block).  One query for each
-// of up to 8 heads: S = K Q^T and O += V^T P on mma.m16n8k16, with keys (dimensions) as the 16
-// rows and the heads as the 8 columns, so that the codes, converted in registers to fp16 (exact),
-// are the large operand and nothing is padded.  tcgen05 has nothing to win here: its operands would
-// have to be converted and written back to shared memory first, and the tile's arithmetic is a
-// quarter of what the legacy instructions do in the time that the codes take to arrive.
+// share of the units (chunks of CK keys of a distinct block).  One query for each of up to 8 heads:
+// S = K Q^T and O += V^T P on mma.m16n8k16, with keys (dimensions) as the 16 rows and the heads as the
+// 8 columns, so that the codes, converted in registers to fp16 (exact), are the large operand.  tcgen05
+// has nothing to win here: its operands would have to be converted and written back to shared memory
+// first, and these instructions are busy for 18 % of the time that the codes take to arrive.
 //  - Q is scaled by a power of two for each head and held in fp16: exact down to 2^-32 of the head's
 //    largest element.
-//  - The value scale enters through the exponent, w_j = 2^(z_j + log2 Vs - M) with M the running
-//    maximum of z_j + log2 Vs: fp16 weights are relative to the largest CONTRIBUTION, however far
-//    the pages' scales lie apart (rounding 2^-11 of each weight).  The sum of the softmax takes
-//    2^(z_j - M) in fp32.
+//  - The value scale enters through the exponent, w_j = 2^(z_j + log2 Vs - M) with M the maximum of
+//    z_j + log2 Vs so far, or up to 8 less: fp16 weights are relative to the largest CONTRIBUTION,
+//    however far the pages' scales lie apart (rounding 2^-11 of each weight).  The sum of the softmax
+//    takes 2^(z_j - M) in fp32.
 //  - The k index of the products runs through a lane's own bytes, so both operands come out of the
 //    swizzled tiles by 16-byte reads without bank conflicts; only the weights change places between
 //    lanes (movmatrix).
@@ -912,7 +909,7 @@ cudaError_t launch_gate(const CacheGeom& g, const __nv_bfloat16* Q, const float*
                         int32_t* sel, const CacheDecodeWork& w, cudaStream_t st) {
   // CTAs of a cluster share the candidates, 64 blocks each at a time
   int c = 1;
-  while (c < 8 && g.k > 1 && c * kGateWarps * kGateRows < g.MB - 1) c *= 2;
+  while (c < 8 && c * kGateWarps * kGateRows < g.MB - 1) c *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)c, (unsigned)g.Hkv, (unsigned)g.B);
   cfg.blockDim = dim3(kGateWarps * 32);
