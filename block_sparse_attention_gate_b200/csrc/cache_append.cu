@@ -14,11 +14,12 @@
 // Bound by HBM for prompts (bf16 in, codes out: 6 bytes for each element of K and V together), by
 // latency for single tokens.  Two forms of one body:
 //   cache_append_kernel : a CTA for each (request, KV head, K or V) takes the request's touched
-//                         pages one after the other: one launch of few CTAs for decode steps (2.7 us
-//                         for 8 requests, 5.8 us for 64 of which some complete a block of 512).
-//   cache_prompt_kernel : a cluster of up to 8 CTAs for each (touched MoBA block, KV head, K or half of V);
-//                         its CTAs share the block's pages and add up the pooled key on the way
-//                         (54769 tokens, 8 heads of 128, pages of 64: 336 MB in 63 us, 5.4 TB/s).
+//                         pages one after the other: for requests with few new tokens (2.7 us for
+//                         single tokens of 8, 5.8 us for 64 of which some complete a block of 512).
+//   cache_prompt_kernel : for requests with the tokens of kLongPages pages or more, a cluster of up to 8
+//                         CTAs for each (touched MoBA block, some KV heads, K or half of V); its CTAs
+//                         share the block's pages and add up the pooled key on the way (54769 tokens, 8
+//                         heads of 128, pages of 64: 336 MB in 63 us, 5.4 TB/s).
 #include <float.h>
 
 #include "cache.cuh"
@@ -29,6 +30,8 @@ namespace {
 
 constexpr int kStepThreads = 256;  // of cache_append_kernel
 constexpr int kMaxWarps = kStepThreads / 32;
+constexpr int kLongPages = 4;
+constexpr int64_t kMostCtas = 8192;  // of a launch of which most may have nothing to do
 constexpr float kTiny = 0x1p-96f;  // keeps scales and quotients far from the subnormal range
 constexpr uint32_t kInfBits = 0x7f80;  // magnitude bits of a bf16 infinity; NaN lies above
 
@@ -322,7 +325,7 @@ __device__ __forceinline__ int32_t page_of_slot(const CacheGeom& g, int32_t slot
 
 template <int kD, int kFmt>
 __global__ void __launch_bounds__(kStepThreads)
-    cache_append_kernel(CacheGeom g, AppendSide sk, AppendSide sv, int32_t max_tokens,
+    cache_append_kernel(CacheGeom g, AppendSide sk, AppendSide sv, int32_t max_tokens, int32_t too_long,
                         const int32_t* __restrict__ cu_new, const int32_t* __restrict__ lens,
                         const int32_t* __restrict__ slots, const int32_t* __restrict__ tables, float* Kbar) {
   __shared__ AppendSmem<kD> sm;
@@ -331,7 +334,7 @@ __global__ void __launch_bounds__(kStepThreads)
   const AppendSide a = is_v ? sv : sk;
   const int32_t t0 = max(__ldg(cu_new + s), 0), t1 = min(__ldg(cu_new + s + 1), max_tokens);
   const int32_t len = cached_len(g, lens, s), n = t1 - t0, start = len - n;
-  if (n <= 0 || start < 0) return;
+  if (n <= 0 || start < 0 || n >= too_long) return;
   int turn = 0;
   for (int32_t pos = start; pos < len;) {
     const int off = pos % g.ps, nr = min(g.ps - off, len - pos);
@@ -378,22 +381,53 @@ __global__ void __launch_bounds__(kStepThreads)
   }
 }
 
-// Work items are numbered so that request s has floor(n / bs) + 2 of them (as many MoBA blocks as n
-// tokens can touch), from floor(cu_new[s] / bs) + 2 s on.
-__device__ __forceinline__ int first_item(int32_t cu, int s, int bs) { return cu / bs + 2 * s; }
+// A long request's new tokens, and which of its touched MoBA blocks a work item is.
+struct LongRun {
+  int32_t s, t0, start, len, block;
+};
 
-// Last request whose items start at or before `item` (a warp narrows the range to 1 / 32 a step).
-__device__ __forceinline__ int request_of_item(const CacheGeom& g, const int32_t* __restrict__ cu_new, int item) {
-  int lo = 0, n = g.B;
-  while (n > 1) {
-    const int step = (n + 31) / 32, x = lo + (int)(threadIdx.x & 31) * step;
-    const bool at = x < lo + n && first_item(max(__ldg(cu_new + min(x, g.B - 1)), 0), x, g.bs) <= item;
-    const int below = __popc(__ballot_sync(0xffffffffu, at));
-    const int next = lo + max(below - 1, 0) * step;
-    n = min(step, lo + n - next);
-    lo = next;
+// Work items are the touched blocks of the long requests, in the order of the requests: a scan of how
+// many each has, a thread a request, until the item's is found (run->s < 0: there are fewer).
+template <int kThreads>
+__device__ __forceinline__ void find_run(const CacheGeom& g, const int32_t* __restrict__ cu_new,
+                                         const int32_t* __restrict__ lens, int32_t max_tokens, int32_t too_short, int item,
+                                         int32_t (*sums)[kThreads / 32], LongRun* run) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) run->s = -1;
+  int32_t before = 0;
+  int turn = 0;
+  for (int s0 = 0; s0 < g.B && before <= item; s0 += kThreads) {
+    const int s = s0 + (int)threadIdx.x;
+    LongRun r{s, 0, 0, 0, 0};
+    int32_t count = 0;
+    if (s < g.B) {
+      r.t0 = max(__ldg(cu_new + s), 0);
+      const int32_t n = min(__ldg(cu_new + s + 1), max_tokens) - r.t0;
+      r.len = cached_len(g, lens, s);
+      r.start = r.len - n;
+      if (n > too_short && r.start >= 0) count = (r.len - 1) / g.bs - r.start / g.bs + 1;
+    }
+    int32_t inc = count;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int32_t o = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += o;
+    }
+    turn ^= 1;  // sums of two rounds ago are read
+    if (lane == 31) sums[turn][warp] = inc;
+    __syncthreads();
+    int32_t at = before + inc - count;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) at += sums[turn][w];
+      before += sums[turn][w];
+    }
+    if (item >= at && item < at + count) {
+      r.block = r.start / g.bs + (item - at);
+      *run = r;
+    }
   }
-  return lo;
+  __syncthreads();
 }
 
 __host__ __device__ constexpr int prompt_threads(int ps) { return ps == 128 ? 256 : 128; }
@@ -401,8 +435,8 @@ __host__ __device__ constexpr int prompt_threads(int ps) { return ps == 128 ? 25
 // kPS: tokens of a page; kAhead: pages on their way while one is written.
 template <int kD, int kFmt, int kPS, int kAhead>
 __global__ void __launch_bounds__(prompt_threads(kPS), kPS == 128 ? 3 : 6)
-    cache_prompt_kernel(CacheGeom g, AppendSide sk, AppendSide sv, int32_t max_tokens, int ranks,
-                        const int32_t* __restrict__ cu_new, const int32_t* __restrict__ lens,
+    cache_prompt_kernel(CacheGeom g, AppendSide sk, AppendSide sv, int32_t max_tokens, int32_t too_short, int ranks,
+                        int heads, const int32_t* __restrict__ cu_new, const int32_t* __restrict__ lens,
                         const int32_t* __restrict__ slots, const int32_t* __restrict__ tables, float* Kbar) {
   constexpr int kPromptThreads = prompt_threads(kPS), kIt = kPS * (kD / 8) / kPromptThreads;
   using Rows = PageRows<kD, kFmt, kIt, kPromptThreads>;
@@ -410,14 +444,14 @@ __global__ void __launch_bounds__(prompt_threads(kPS), kPS == 128 ? 3 : 6)
   g.ps = kPS;
   __shared__ AppendSmem<kD> sm;
   extern __shared__ __align__(16) uint8_t stages[];
-  const int item = blockIdx.x / ranks, rank = blockIdx.x % ranks, head = blockIdx.y;
+  const int item = blockIdx.x / ranks, rank = blockIdx.x % ranks;
   const bool is_v = blockIdx.z != 0;
   const AppendSide a = is_v ? sv : sk;
-  const int s = request_of_item(g, cu_new, item);
-  const int32_t t0 = max(__ldg(cu_new + s), 0), t1 = min(__ldg(cu_new + s + 1), max_tokens);
-  const int32_t len = cached_len(g, lens, s), n = t1 - t0, start = len - n;
-  const int b = start / g.bs + (item - first_item(t0, s, g.bs));
-  if (n <= 0 || start < 0 || b < 0 || (int64_t)b * g.bs >= len) return;  // the same for the whole cluster
+  __shared__ LongRun run;
+  __shared__ int32_t sums[2][kPromptThreads / 32];
+  find_run<kPromptThreads>(g, cu_new, lens, max_tokens, too_short, item, sums, &run);
+  const int32_t s = run.s, t0 = run.t0, start = run.start, len = run.len, b = run.block;
+  if (s < 0) return;  // the same for the whole cluster
   const bool pool = !is_v && (int64_t)(b + 1) * g.bs <= len;
   const int R = g.bs / g.ps, per = (R + ranks - 1) / ranks;
   int p0 = b * R + rank * per, p1 = b * R + min(R, (rank + 1) * per);
@@ -425,7 +459,6 @@ __global__ void __launch_bounds__(prompt_threads(kPS), kPS == 128 ? 3 : 6)
     const int half = (max(p1 - p0, 0) + 1) / 2;
     if (blockIdx.z == 1) p1 = min(p1, p0 + half); else p0 += half;
   }
-  const __nv_bfloat16* src = a.src + (size_t)head * kD;
   // new rows of page ordinal p: packed row of the first, how many, and the older rows before them
   auto rows_of = [&](int p, int32_t& t, int& nr, int& off) {
     const int32_t lo = max(start, p * g.ps), hi = min(len, (p + 1) * g.ps);
@@ -434,13 +467,7 @@ __global__ void __launch_bounds__(prompt_threads(kPS), kPS == 128 ? 3 : 6)
     nr = p < p1 ? max(hi - lo, 0) : 0;
   };
   const uint32_t ring = smem_u32(stages);
-  auto prefetch = [&](int p, int stage) {
-    int32_t t;
-    int nr, off;
-    rows_of(p, t, nr, off);
-    if (nr > 0) Rows::prefetch(ring + stage * kStageBytes, src + (int64_t)t * a.stride, a.stride, nr);
-    cp_async_commit();
-  };
+  int turn = 0;
   // slot of a page's first new token, and the page that the block table names (the pooled key is that of
   // these pages), read one page ahead and looked at only when it is their turn
   auto slot_of = [&](int p) -> int32_t {
@@ -450,70 +477,86 @@ __global__ void __launch_bounds__(prompt_threads(kPS), kPS == 128 ? 3 : 6)
     return nr > 0 ? __ldg(slots + t) : -1;
   };
   auto listed_at = [&](int p) -> int32_t { return pool && p < p1 ? __ldg(tables + (size_t)s * g.MP + p) : -1; };
+  for (int head = blockIdx.y * heads; head < min(g.Hkv, (int)(blockIdx.y + 1) * heads); ++head) {
+    const __nv_bfloat16* src = a.src + (size_t)head * kD;
+    auto prefetch = [&](int p, int stage) {
+      int32_t t;
+      int nr, off;
+      rows_of(p, t, nr, off);
+      if (nr > 0) Rows::prefetch(ring + stage * kStageBytes, src + (int64_t)t * a.stride, a.stride, nr);
+      cp_async_commit();
+    };
 #pragma unroll
-  for (int q = 0; q < kAhead; ++q) prefetch(p0 + q, q);
-  int turn = 0, stage = 0;
-  int32_t slot = slot_of(p0), listed = listed_at(p0);
-  float acc[8] = {};
-  for (int p = p0; p < p1; ++p) {
-    prefetch(p + kAhead, stage == 0 ? kAhead : stage - 1);  // the stage that the last page left
-    const int32_t slot_n = slot_of(p + 1), listed_n = listed_at(p + 1);
-    int32_t t;
-    int nr, off;
-    rows_of(p, t, nr, off);
-    const int32_t page = page_of_slot(g, slot, off);
-    if (pool && !page_ok(g, listed)) {
-      if (threadIdx.x == 0) atomicOr(g.err, kErrBadPage);
-      listed = -1;
-    }
-    cp_async_wait<kAhead>();
-    Rows rows;
-    if (page >= 0) rows.take(ring + stage * kStageBytes);
-    float* sp = a.scales + (size_t)max(page, 0) * g.Hkv + head;
-    uint8_t* slab = a.codes + slab_offset(g, max(page, 0), head);
-    if (pool && page >= 0 && page == listed && off == 0) {
-      CodeSums<kFmt, 8> sum;
-      const float scale = rows.template store<true>(nr, off, slab, sp, sm.red, turn, sum);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = fmaf(sum.sum(e), scale, acc[e]);
-    } else {
-      CodeSums<kFmt, 8> unused;
-      if (page >= 0) rows.template store<false>(nr, off, slab, sp, sm.red, turn, unused);
-      if (pool) {  // older rows are in the page: read all of it back
-        __syncthreads();
-        if (listed >= 0)
-          add_stored_page<kD, kFmt, kPromptThreads>(g, a.codes + slab_offset(g, listed, head),
-                                                    a.scales[(size_t)listed * g.Hkv + head], acc);
+    for (int q = 0; q < kAhead; ++q) prefetch(p0 + q, q);
+    int stage = 0;
+    int32_t slot = slot_of(p0), listed = listed_at(p0);
+    float acc[8] = {};
+    for (int p = p0; p < p1; ++p) {
+      prefetch(p + kAhead, stage == 0 ? kAhead : stage - 1);  // the stage that the last page left
+      const int32_t slot_n = slot_of(p + 1), listed_n = listed_at(p + 1);
+      int32_t t;
+      int nr, off;
+      rows_of(p, t, nr, off);
+      const int32_t page = page_of_slot(g, slot, off);
+      if (pool && !page_ok(g, listed)) {
+        if (threadIdx.x == 0) atomicOr(g.err, kErrBadPage);
+        listed = -1;
       }
+      cp_async_wait<kAhead>();
+      Rows rows;
+      if (page >= 0) rows.take(ring + stage * kStageBytes);
+      float* sp = a.scales + (size_t)max(page, 0) * g.Hkv + head;
+      uint8_t* slab = a.codes + slab_offset(g, max(page, 0), head);
+      if (pool && page >= 0 && page == listed && off == 0) {
+        CodeSums<kFmt, 8> sum;
+        const float scale = rows.template store<true>(nr, off, slab, sp, sm.red, turn, sum);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = fmaf(sum.sum(e), scale, acc[e]);
+      } else {
+        CodeSums<kFmt, 8> unused;
+        if (page >= 0) rows.template store<false>(nr, off, slab, sp, sm.red, turn, unused);
+        if (pool) {  // older rows are in the page: read all of it back
+          __syncthreads();
+          if (listed >= 0)
+            add_stored_page<kD, kFmt, kPromptThreads>(g, a.codes + slab_offset(g, listed, head),
+                                                      a.scales[(size_t)listed * g.Hkv + head], acc);
+        }
+      }
+      slot = slot_n;
+      listed = listed_n;
+      stage = stage == kAhead ? 0 : stage + 1;
     }
-    slot = slot_n;
-    listed = listed_n;
-    stage = stage == kAhead ? 0 : stage + 1;
+    if (!pool) continue;  // the same for the whole cluster
+    fold_columns<kD, 8, kPromptThreads>(acc, sm);
+    cluster_barrier();
+    if (rank == 0 && threadIdx.x < kD) {
+      float total = sm.part[threadIdx.x];
+      for (int r = 1; r < ranks; ++r) total += ld_cluster_f32(&sm.part[threadIdx.x], r);
+      Kbar[(((size_t)s * g.MB + b) * g.Hkv + head) * kD + threadIdx.x] = total / (float)g.bs;
+    }
+    cluster_barrier();  // no CTA goes on while its share is read
   }
-  if (!pool) return;  // the same for the whole cluster
-  fold_columns<kD, 8, kPromptThreads>(acc, sm);
-  cluster_barrier();
-  if (rank == 0 && threadIdx.x < kD) {
-    float total = sm.part[threadIdx.x];
-    for (int r = 1; r < ranks; ++r) total += ld_cluster_f32(&sm.part[threadIdx.x], r);
-    Kbar[(((size_t)s * g.MB + b) * g.Hkv + head) * kD + threadIdx.x] = total / (float)g.bs;
-  }
-  cluster_barrier();  // no CTA leaves while its share is read
 }
 
 template <int kD, int kFmt, int kPS, int kAhead>
 cudaError_t launch_prompt(const CacheGeom& g, const AppendSide& sk, const AppendSide& sv, int32_t max_tokens,
-                          const int32_t* cu_new, const int32_t* lens, const int32_t* slots, const int32_t* tables,
-                          float* Kbar, cudaStream_t st) {
+                          int32_t too_short, const int32_t* cu_new, const int32_t* lens, const int32_t* slots,
+                          const int32_t* tables, float* Kbar, cudaStream_t st) {
+  // n tokens touch at most n / bs + 2 blocks
+  const int64_t runs = too_short > 0 ? max_tokens / (too_short + 1) : g.B;
+  const int64_t items = max_tokens / g.bs + 2 * (runs < g.B ? runs : g.B);
   // CTAs of a cluster: at least 128 rows each, and at most 4 once there are several rounds of CTAs (each
   // begins with a few loads one behind the other, which longer runs of pages spread): prompts of 128K
   // tokens took 77 us with 4, 80 with 8 and 82 with 2; 8K tokens 6.8 with 8 and 8.2 with 4
-  const int64_t items = max_tokens / g.bs + 2 * (int64_t)g.B;
   const int most = items * g.Hkv * 2 * 8 > 4 * 148 * 6 ? 4 : 8;
   int ranks = 1;
   while (ranks < most && 2 * ranks * 128 <= g.bs) ranks *= 2;
+  // heads of a CTA: one, but more where most of the items may turn out not to be there, as even an empty
+  // CTA takes 1.5 ns to start
+  int heads = 1;
+  while (heads < g.Hkv && items * ranks * ((g.Hkv + heads - 1) / heads) * 3 > kMostCtas) heads *= 2;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(items * ranks), (unsigned)g.Hkv, 3);
+  cfg.gridDim = dim3((unsigned)(items * ranks), (unsigned)((g.Hkv + heads - 1) / heads), 3);
   cfg.blockDim = dim3(prompt_threads(kPS));
   cfg.dynamicSmemBytes = (kAhead + 1) * kPS * kD * 2;
   cfg.stream = st;
@@ -525,7 +568,8 @@ cudaError_t launch_prompt(const CacheGeom& g, const AppendSide& sk, const Append
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_prompt_kernel<kD, kFmt, kPS, kAhead>, g, sk, sv, max_tokens, ranks, cu_new, lens, slots,
+  return cudaLaunchKernelEx(&cfg, cache_prompt_kernel<kD, kFmt, kPS, kAhead>, g, sk, sv, max_tokens, too_short, ranks,
+                            heads, cu_new, lens, slots,
                             tables, Kbar);
 }
 
@@ -533,13 +577,22 @@ template <int kD, int kFmt>
 cudaError_t launch_append_t(const CacheGeom& g, const AppendSide& sk, const AppendSide& sv, int32_t max_tokens,
                             const int32_t* cu_new, const int32_t* lens, const int32_t* slots, const int32_t* tables,
                             float* Kbar, cudaStream_t st) {
-  // A few tokens for each slot (decode steps, drafts): one CTA a request, no empty clusters to start.
-  if (max_tokens <= 4 * (int64_t)g.B) {
+  // Where a request has two pages of new tokens on average, all go as prompts; else those with fewer than
+  // kLongPages one page after the other and then the others, where there can be any (with up to 4 tokens
+  // a slot, as decode steps and drafts have, there hardly are).  64 requests with 16 tokens each take 11
+  // us in two launches and 39 us as prompts, most of it empty clusters; 8 with 256 tokens 15 and 13 us; one
+  // with 8000 beside 63 with one 26 and 46 us, and over 100 us one page after the other.
+  const int32_t tokens = kLongPages * g.ps;
+  const bool prompts = max_tokens >= 2 * (int64_t)g.ps * g.B;
+  const bool few = max_tokens < tokens || max_tokens <= 4 * (int64_t)g.B;
+  if (!prompts) {
     cache_append_kernel<kD, kFmt><<<dim3((unsigned)g.Hkv, (unsigned)g.B, 2), kStepThreads, 0, st>>>(
-        g, sk, sv, max_tokens, cu_new, lens, slots, tables, Kbar);
-    return cudaGetLastError();
+        g, sk, sv, max_tokens, few ? INT32_MAX : tokens, cu_new, lens, slots, tables, Kbar);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || few) return e;
   }
-  auto go = [&](auto fn) { return fn(g, sk, sv, max_tokens, cu_new, lens, slots, tables, Kbar, st); };
+  const int32_t too_short = prompts ? 0 : tokens - 1;
+  auto go = [&](auto fn) { return fn(g, sk, sv, max_tokens, too_short, cu_new, lens, slots, tables, Kbar, st); };
   switch (g.ps) {  // 24 to 64 KB of shared memory: 3 or more CTAs on an SM
     case 16: return go(launch_prompt<kD, kFmt, 16, 4>);
     case 32: return go(launch_prompt<kD, kFmt, 32, 2>);

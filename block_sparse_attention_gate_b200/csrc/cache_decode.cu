@@ -959,9 +959,10 @@ cudaError_t launch_decode_t(const CacheGeom& g, const __nv_bfloat16* Q, const ui
                     cache_attn_kernel<kD, kFmt>, tk, tv, g, Q, Ks, Vs, lens, tables, w, g.B * g.Hkv * ((g.G + 7) / 8),
                     own_only);
   if (e != cudaSuccess) return e;
-  // many parts: all warps of a CTA on one row (a warp has eight rows on their way at a time)
+  // All warps of a CTA on one row while every row's are on the GPU at once, else a warp for each: 512 rows of
+  // 8 parts 45.7 us for the step with 8 warps, 47.7 with one; 4096 rows of 9 parts 140 and 127.
   const int64_t rows = (int64_t)g.B * g.Hq;
-  if (g.k * w.NC > 8)
+  if (rows * kMergeWarps <= sms * 64)
     return launch_kernel(true, dim3((unsigned)rows), kMergeWarps * 32, 0, st, cache_merge_kernel<kD, kMergeWarps>, g, lens,
                          w, own_only, sel, O, LSE);
   return launch_kernel(true, dim3((unsigned)((rows + kMergeWarps - 1) / kMergeWarps)), kMergeWarps * 32, 0, st,

@@ -190,8 +190,9 @@ cudaError_t launch_cache_tables(const CacheGeom& g, const int32_t* add, const in
                                 int32_t* free_pages, const int32_t* free_state, int32_t* lens_out,
                                 int32_t* free_state_out, int32_t* cu_new, int32_t* slots, int32_t max_tokens,
                                 int32_t* status, cudaStream_t st) {
-  // one CTA writes a decode step's slots at once; a prompt's are worth a cluster
-  const unsigned c = max_tokens > 2 * kTabThreads ? 8 : 1;
+  // one CTA writes a decode step's slots at once; a prompt's are worth a cluster: 64 requests with 64, 1024,
+  // 2048 and 4096 tokens take 4.2, 4.5, 5.3 and 6.7 us with one, 4.5, 4.9, 4.9 and 4.9 with 8
+  const unsigned c = max_tokens > kTabThreads ? 8 : 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(c);
   cfg.blockDim = dim3(kTabThreads);

@@ -229,7 +229,7 @@ def _append_case(rng, p, pool, old, add, N, kv, fmt, ps, bs, D, H, kbar):
 @pytest.mark.parametrize("B,max_len,ps,H,D,bs,new", [
     (1, 1, 16, 1, 64, 128, 1), (5, 300, 32, 2, 64, 128, 1), (4, 700, 128, 3, 128, 256, 9), (3, 1500, 64, 2, 128, 384, 700),
     (2, 1030, 16, 1, 128, 128, 900), (9, 400, 16, 8, 64, 128, 60), (1, 2300, 128, 2, 128, 1024, 2300),
-    (40, 130, 32, 1, 64, 128, 2)])
+    (40, 130, 32, 1, 64, 128, 2), (300, 220, 16, 1, 64, 128, 200), (140, 600, 32, 2, 128, 256, 400)])
 def test_append(B, max_len, ps, H, D, bs, new, fmt, cuda_device):
     import torch
     rng = np.random.default_rng(B * 7 + new)
@@ -249,6 +249,27 @@ def test_append(B, max_len, ps, H, D, bs, new, fmt, cuda_device):
     kv = _bf16(kv)
     kbar = torch.full((B, p.max_blocks, H, D), 7.0, device="cuda")
     _append_case(rng, p, pool, old, add, N, (kv[:, 0], kv[:, 1]), fmt, ps, bs, D, H, kbar)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("ps,D,H,bs", [(32, 64, 2, 128), (16, 128, 5, 256), (64, 128, 1, 512), (128, 64, 3, 384)])
+def test_append_long_runs_beside_short_ones(ps, D, H, bs, fmt, cuda_device):
+    """Requests with a long prompt, at and around four pages, with single tokens and with none, in one call."""
+    import torch
+    rng = np.random.default_rng(ps)
+    B, max_len = 150, 1500
+    add = rng.integers(0, 3, B)
+    for s, n in zip((3, 40, 41, 129, 149), (1100, 4 * ps, 4 * ps - 1, 4 * ps + 1, 2 * ps)):
+        add[s] = n
+    old = np.array([rng.integers(0, min(max_len - a, 400) + 1) for a in add])
+    N = int(add.sum()) + 3
+    assert 4 * ps <= N < 2 * ps * B and N > 4 * B  # two launches
+    P = B * -(-max_len // ps)
+    p = _mb().MobaCacheParams(B, max_len, P, ps, H, H, D, bs, 1, fmt)
+    pool = Pool(rng, B, max_len, P, ps, H, D, fmt)
+    kv = _bf16(rng.standard_normal((N, 2, H, D)) * np.exp(rng.standard_normal((N, 1, 1, 1))))
+    kbar = torch.full((B, p.max_blocks, H, D), 7.0, device="cuda")
+    assert _append_case(rng, p, pool, old, add, N, (kv[:, 0], kv[:, 1]), fmt, ps, bs, D, H, kbar) > 2
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
