@@ -6,8 +6,9 @@
 //   table[s][h_s + j] = ring[(head + off_s + j) mod P],            j < g_s
 //   slot[cu_new_s + j] = table[s][(len_s + j) / ps] * ps + (len_s + j) mod ps,
 // and the pages of a request that ends (add_s < 0) go behind the ring's last free page.  The ring
-// is a queue: what a call takes (front) and what it gives back (behind the end) never overlap, so
-// nothing has to be ordered between the two and the results do not depend on timing.
+// is a queue: what a call takes (front) and what it gives back (behind the end) do not overlap where
+// the free pages and those given back are no more than the pool, and a call for which they are more
+// is refused.  So nothing has to be ordered between the two and the results do not depend on timing.
 //
 // Latency bound: a few bytes per request.  Every CTA of a cluster scans all requests (in chunks of its
 // size; several chunks take a first pass for the totals, which decide whether the call changes
@@ -131,7 +132,8 @@ __global__ void __launch_bounds__(kTabThreads)
   bad = (__syncthreads_or(bad & kTabState) ? kTabState : 0) | (__syncthreads_or(bad & kTabTooLong) ? kTabTooLong : 0);
   if ((uint32_t)head >= P || (uint32_t)count > P) bad |= kTabState;
   else if (total.need > count) bad |= kTabNoPages;
-  else if ((int64_t)count - total.need + total.back > g.P) bad |= kTabState;
+  // what comes back has to fit beside all of the free pages: those that are taken are read meanwhile
+  else if ((int64_t)count + total.back > g.P) bad |= kTabState;
   if (total.n > max_tokens) bad |= kTabSlots;
   const bool go = bad == 0;
   // ---- pages and tokens

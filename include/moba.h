@@ -327,9 +327,10 @@ typedef struct {
  *          (-1 too where the ring held a page id outside the pool).
  *   status [1] out: 0, or the sum of 1 (too few free pages), 2 (a request would exceed
  *          max_seqlen), 4 (more new tokens than max_tokens), 8 (a length or free_state outside
- *          its range, or more pages given back than the ring has room for).  With a status other
- *          than 0 nothing changes: lens_out = lens, free_state_out = free_state, cu_new is all 0
- *          and slots all -1, so that the append that follows writes nothing.
+ *          its range, or the free pages and those given back are more than the pool: pages that
+ *          are taken make no room, as they are read in the same call).  With a status other than
+ *          0 nothing changes: lens_out = lens, free_state_out = free_state, cu_new is all 0 and
+ *          slots all -1, so that the append that follows writes nothing.
  * lens_out may be lens and free_state_out may be free_state (in place); other buffers must not
  * overlap.  All values are exact and do not depend on timing.
  */
