@@ -7,8 +7,9 @@
 //   slot[cu_new_s + j] = table[s][(len_s + j) / ps] * ps + (len_s + j) mod ps,
 // and the pages of a request that ends (add_s < 0) go behind the ring's last free page.  The ring
 // is a queue: what a call takes (front) and what it gives back (behind the end) do not overlap where
-// the free pages and those given back are no more than the pool, and a call for which they are more
-// is refused.  So nothing has to be ordered between the two and the results do not depend on timing.
+// the free pages and those held are no more than the pool, and a call for which they are more is
+// refused: some page is then listed twice.  So nothing has to be ordered between the two and the
+// results do not depend on timing.
 //
 // Latency bound: a few bytes per request.  Every CTA of a cluster scans all requests (in chunks of its
 // size; several chunks take a first pass for the totals, which decide whether the call changes
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(kTabThreads)
                         int32_t* slots, int32_t max_tokens, int32_t* status) {
   __shared__ Triple warp_sums[kTabThreads / 32];
   __shared__ int32_t s_tok[kTabThreads], s_need[kTabThreads], s_back[kTabThreads];  // chunk offsets
-  __shared__ int32_t s_len[kTabThreads];
+  __shared__ int32_t s_len[kTabThreads], s_held[kTabThreads / 32];
   const int tid = threadIdx.x, rank = blockIdx.x, lps = 31 - __clz(g.ps);
   const bool one = g.B <= kTabThreads;  // a single chunk
   const int32_t first = rank * kTabThreads + tid, step = gridDim.x * kTabThreads;  // of pages and tokens
@@ -122,18 +123,24 @@ __global__ void __launch_bounds__(kTabThreads)
   Triple total{0, 0, 0}, off{0, 0, 0}, t{0, 0, 0};
   Growth r;
   int bad = 0;
+  int32_t held = 0;  // pages of all requests: at most the entries of the block tables
   for (int b0 = 0; b0 < g.B; b0 += kTabThreads) {
     r = growth_of(g, lps, add, lens, b0 + tid);
     bad |= r.bad;
+    held += r.have;
     off = block_scan({r.n, r.need, r.back}, warp_sums, &t);
     total = add3(total, t);
   }
+  held = __reduce_add_sync(0xffffffffu, held);
+  if ((tid & 31) == 0) s_held[tid >> 5] = held;
   // the four bits of all threads
   bad = (__syncthreads_or(bad & kTabState) ? kTabState : 0) | (__syncthreads_or(bad & kTabTooLong) ? kTabTooLong : 0);
+  held = __reduce_add_sync(0xffffffffu, s_held[tid & 31]);
   if ((uint32_t)head >= P || (uint32_t)count > P) bad |= kTabState;
   else if (total.need > count) bad |= kTabNoPages;
-  // what comes back has to fit beside all of the free pages: those that are taken are read meanwhile
-  else if ((int64_t)count + total.back > g.P) bad |= kTabState;
+  // more pages than there are: what comes back might overrun the free pages, which are read meanwhile, and a
+  // page that two requests hold would come back while one of them still reads it
+  else if ((int64_t)count + held > g.P) bad |= kTabState;
   if (total.n > max_tokens) bad |= kTabSlots;
   const bool go = bad == 0;
   // ---- pages and tokens

@@ -284,9 +284,12 @@ MOBA_API moba_status moba_fwd_host(const moba_params* p, const void* Q, const vo
  * kind before the first capture).  Int32 buffers need 4-byte alignment, everything else 16.  A
  * captured call uses the buffers it was captured with: two graphs that share a workspace, or a
  * cache, must not run at the same time.
- * Scales are positive and finite, as moba_cache_append writes them.  Requests may share pages that
- * are only read (equal entries of their rows); a page that is written belongs to one request.  A
- * request only grows or ends: it is not cut back.
+ * Scales are positive and finite, as moba_cache_append writes them.  A page belongs to one request:
+ * moba_cache_tables takes all pages of a request back when it ends, so the rows that it serves must
+ * not share any.  (moba_cache_decode_fwd, and moba_cache_append for pages that it does not write,
+ * only read through the rows: a caller who keeps the tables without moba_cache_tables may let rows
+ * share pages there.  Kbar belongs to each request alone.)  A request only grows or ends: it is not
+ * cut back.
  *
  * A page id outside [0, num_pages), a length outside [0, max_seqlen] and a slot that does not
  * fit its token never lead to an access: such tokens are left out (read as masked, not written),
@@ -327,10 +330,10 @@ typedef struct {
  *          (-1 too where the ring held a page id outside the pool).
  *   status [1] out: 0, or the sum of 1 (too few free pages), 2 (a request would exceed
  *          max_seqlen), 4 (more new tokens than max_tokens), 8 (a length or free_state outside
- *          its range, or the free pages and those given back are more than the pool: pages that
- *          are taken make no room, as they are read in the same call).  With a status other than
- *          0 nothing changes: lens_out = lens, free_state_out = free_state, cu_new is all 0 and
- *          slots all -1, so that the append that follows writes nothing.
+ *          its range, or the free pages and those that the requests hold before the call are more
+ *          than the pool, so that some page is listed twice).  With a status other than 0 nothing
+ *          changes: lens_out = lens, free_state_out = free_state, cu_new is all 0 and slots all
+ *          -1, so that the append that follows writes nothing.
  * lens_out may be lens and free_state_out may be free_state (in place); other buffers must not
  * overlap.  All values are exact and do not depend on timing.
  */
