@@ -113,7 +113,7 @@ moba::CacheDecodeWork carve_cache_decode(const moba::CacheGeom& g, char* base) {
   w.segs = (moba::CacheSeg*)take(entries * w.max_segs * sizeof(moba::CacheSeg));
   w.units = (int32_t*)take(entries * sizeof(int32_t));
   w.part_o = (float*)take(parts * g.D * sizeof(float));
-  w.part_ml = (float2*)take(parts * sizeof(float2));
+  w.part_ml = (float4*)take(parts * sizeof(float4));
   w.sel = (int32_t*)take(rows * g.k * sizeof(int32_t));
   w.bytes = off;
   return w;

@@ -239,7 +239,8 @@ __global__ void __launch_bounds__(kGateWarps * 32)
 //  - The value scale enters through the exponent, w_j = 2^(z_j + log2 Vs - M) with M the maximum of
 //    z_j + log2 Vs so far, or up to 8 less: fp16 weights are relative to the largest CONTRIBUTION,
 //    however far the pages' scales lie apart (rounding 2^-11 of each weight).  The sum of the softmax
-//    takes 2^(z_j - M) in fp32.
+//    takes 2^(z_j - R) in fp32, with R the maximum of z_j so far, or up to 8 less: log2 Vs may lie
+//    anywhere from -105 (a page of zeros) to 121, so relative to M the sum would overflow or vanish.
 //  - The k index of the products runs through a lane's own bytes, so both operands come out of the
 //    swizzled tiles by 16-byte reads without bank conflicts; only the weights change places between
 //    lanes (movmatrix).
@@ -248,6 +249,7 @@ __global__ void __launch_bounds__(kGateWarps * 32)
 // conversions and the softmax of half as many bytes a key bound it: 156 MB of 37 ragged int8 caches in
 // 45 us, issue slots 48 % busy.
 
+constexpr float kNoScore = -1e38f;  // reference before the first key: finite, below every score that counts
 constexpr int kPiece = 256;     // keys whose pages a warp holds at a time (at most 16 pages)
 
 template <int kD>
@@ -544,8 +546,8 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
   uint32_t qb[kW][2];
   float sf[2];                  // of heads 2t, 2t + 1: softmax scale over Q's power of two, log2 units
   int q_idx = -1;
-  float o[kW][4], m[2], l[2];   // m: reference of the weights (below); l: sum of the softmax
-  float base[2], limit[2];      // m, or 0 before the first key; the largest score that m serves
+  float o[kW][4], l[2];         // l: sum of the softmax
+  float m[2], r[2];             // references of the weights in o and of those in l (below)
   bool fresh = true;            // nothing is added up yet
 
   while (true) {
@@ -584,8 +586,8 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
       for (int j = 0; j < kW; ++j)
 #pragma unroll
         for (int x = 0; x < 4; ++x) o[j][x] = 0.f;
-      m[0] = m[1] = limit[0] = limit[1] = -INFINITY;
-      l[0] = l[1] = base[0] = base[1] = 0.f;
+      m[0] = m[1] = r[0] = r[1] = kNoScore;
+      l[0] = l[1] = 0.f;
       fresh = true;
     }
     const float lvs = log2f(vs);
@@ -671,21 +673,33 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
         mx0 = max3(mx0, score(mt, 0, lv[mt]), score(mt, 2, lv[mt]));
         mx1 = max3(mx1, score(mt, 1, lv[mt]), score(mt, 3, lv[mt]));
       }
-      // m is a maximum of earlier keys, not the largest so far: weights up to 2^kSlack are as good in fp16
-      // and fp32, and the exact maximum over the lanes is only needed when a key leaves that range
+      // m and r are maxima of earlier keys, not the largest so far: weights up to 2^kSlack are as good in fp16
+      // and fp32, and the exact maxima over the lanes are only needed when a key leaves that range.  A tile's
+      // largest z is at most its largest z + lv less its smallest lv.
       constexpr float kSlack = 8.f;
-      if (__any_sync(0xffffffffu, mx0 > limit[0] || mx1 > limit[1])) {
+      const float lv_min = kMT > 1 && box != kTile ? fminf(lv[0], lv[kMT - 1]) : lv[0];
+      if (__any_sync(0xffffffffu, mx0 > fminf(m[0], r[0] + lv_min) + kSlack || mx1 > fminf(m[1], r[1] + lv_min) + kSlack)) {
+        float zx0 = -INFINITY, zx1 = -INFINITY;
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt) {
+          zx0 = max3(zx0, score(mt, 0, 0.f), score(mt, 2, 0.f));
+          zx1 = max3(zx1, score(mt, 1, 0.f), score(mt, 3, 0.f));
+        }
 #pragma unroll
         for (int off = 4; off <= 16; off <<= 1) {
           mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
           mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
+          zx0 = fmaxf(zx0, __shfl_xor_sync(0xffffffffu, zx0, off));
+          zx1 = fmaxf(zx1, __shfl_xor_sync(0xffffffffu, zx1, off));
         }
         mx0 = fmaxf(mx0, m[0]);
         mx1 = fmaxf(mx1, m[1]);
+        zx0 = fmaxf(zx0, r[0]);
+        zx1 = fmaxf(zx1, r[1]);
         if (!fresh) {
-          const float a0 = mx0 == -INFINITY ? 0.f : ex2(m[0] - mx0), a1 = mx1 == -INFINITY ? 0.f : ex2(m[1] - mx1);
-          l[0] *= a0;
-          l[1] *= a1;
+          const float a0 = ex2(m[0] - mx0), a1 = ex2(m[1] - mx1);
+          l[0] *= ex2(r[0] - zx0);
+          l[1] *= ex2(r[1] - zx1);
 #pragma unroll
           for (int j = 0; j < kW; ++j) {
             o[j][0] *= a0;
@@ -696,19 +710,16 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
         }
         m[0] = mx0;
         m[1] = mx1;
-        base[0] = mx0 == -INFINITY ? 0.f : mx0;
-        base[1] = mx1 == -INFINITY ? 0.f : mx1;
-        limit[0] = mx0 + kSlack;
-        limit[1] = mx1 + kSlack;
+        r[0] = zx0;
+        r[1] = zx1;
       }
       fresh = false;
-      const float b0 = base[0], b1 = base[1];
       // ---- O += V^T P: dimensions of group gq, heads 2t and 2t + 1
 #pragma unroll
       for (int mt = 0; mt < kMT; ++mt) {
-        l[0] += ex2(score(mt, 0, -b0)) + ex2(score(mt, 2, -b0));
-        l[1] += ex2(score(mt, 1, -b1)) + ex2(score(mt, 3, -b1));
-        const float w0 = lv[mt] - b0, w1 = lv[mt] - b1;
+        l[0] += ex2(score(mt, 0, -r[0])) + ex2(score(mt, 2, -r[0]));
+        l[1] += ex2(score(mt, 1, -r[1])) + ex2(score(mt, 3, -r[1]));
+        const float w0 = lv[mt] - m[0], w1 = lv[mt] - m[1];
         const uint32_t p0 = transpose8(pack_half2(ex2(score(mt, 0, w0)), ex2(score(mt, 1, w1))));
         const uint32_t p1 = transpose8(pack_half2(ex2(score(mt, 2, w0)), ex2(score(mt, 3, w1))));
         if constexpr (kOdd) {
@@ -761,7 +772,7 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
           float4* dst = reinterpret_cast<float4*>(w.part_o + part * kD + gq * (kD / 8));
 #pragma unroll
           for (int j = 0; j < kW; j += 2) dst[j / 2] = make_float4(o[j][e], o[j][2 + e], o[j + 1][e], o[j + 1][2 + e]);
-          if (gq == 0) w.part_ml[part] = make_float2(m[e], ls[e]);
+          if (gq == 0) w.part_ml[part] = make_float4(m[e], r[e], ls[e], 0.f);
         }
       }
     }
@@ -805,7 +816,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   const int own = len > 0 ? (len - 1) / g.bs : 0, own_chunks = (len - own * g.bs + w.CK - 1) / w.CK;
   const int n = own_chunks + min(g.k - 1, own) * w.NC;  // slots are filled from the front
   const int mine = n > part ? (n - part + kWarps - 1) / kWarps : 0;  // parts of this warp
-  const float2* ml = w.part_ml + row * g.k * w.NC;
+  const float4* ml = w.part_ml + row * g.k * w.NC;
   const float* po = w.part_o + row * g.k * w.NC * kD + lane * kDL;
   auto at = [&](int x) { return x < own_chunks ? x : w.NC + (x - own_chunks); };
   float f[kMergeRows][kDL];
@@ -825,20 +836,26 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   };
   wait_for_primary();
   fetch(0);  // while the weights are found
-  float M = -INFINITY;
-  for (int x = lane; x < n; x += 32) M = fmaxf(M, __ldcg(ml + at(x)).x);
+  float M = kNoScore, R = kNoScore;
+  for (int x = lane; x < n; x += 32) {
+    const float4 v = __ldcg(ml + at(x));
+    M = fmaxf(M, v.x);
+    R = fmaxf(R, v.y);
+  }
 #pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  const float base = M == -INFINITY ? 0.f : M;
+  for (int off = 16; off >= 1; off >>= 1) {
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    R = fmaxf(R, __shfl_xor_sync(0xffffffffu, R, off));
+  }
   float L = 0.f, acc[kDL];
 #pragma unroll
   for (int d = 0; d < kDL; ++d) acc[d] = 0.f;
   for (int x0 = 0; x0 < mine; x0 += 32) {
     float wt = 0.f;
     if (x0 + lane < mine) {
-      const float2 v = __ldcg(ml + at(part + (x0 + lane) * kWarps));
-      wt = ex2(v.x - base);
-      L = fmaf(v.y, wt, L);
+      const float4 v = __ldcg(ml + at(part + (x0 + lane) * kWarps));
+      wt = ex2(v.x - M);
+      L = fmaf(v.z, ex2(v.y - R), L);
     }
     for (int x1 = x0; x1 < min(mine, x0 + 32); x1 += kMergeRows) {
       if (x1 > 0) fetch(x1);
@@ -868,10 +885,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   }
   if (!live) return;
   const float inv = L == 0.f ? 0.f : 1.f / L;  // 0: no key at all
+  const float up = ex2(0.5f * (M - R));  // root of what the weights of acc carry of the value scales (up to 2^129)
 #pragma unroll
   for (int d = 0; d < kDL; d += 2)
-    *reinterpret_cast<__nv_bfloat162*>(O + row * kD + lane * kDL + d) = __floats2bfloat162_rn(acc[d] * inv, acc[d + 1] * inv);
-  if (lane == 0) LSE[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2C;
+    *reinterpret_cast<__nv_bfloat162*>(O + row * kD + lane * kDL + d) =
+        __floats2bfloat162_rn(acc[d] * inv * up * up, acc[d + 1] * inv * up * up);
+  if (lane == 0) LSE[row] = L == 0.f ? -INFINITY : (R + log2f(L)) * kLn2C;
   if (own_only && lane < g.k) sel[row * g.k + lane] = lane == 0 && len > 0 ? own : -1;  // there was no gate
 }
 
