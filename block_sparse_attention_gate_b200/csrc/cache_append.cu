@@ -33,6 +33,9 @@ constexpr int kMaxWarps = kStepThreads / 32;
 constexpr int kLongPages = 4;
 constexpr int64_t kMostCtas = 8192;  // of a launch of which most may have nothing to do
 constexpr float kTiny = 0x1p-96f;  // keeps scales and quotients far from the subnormal range
+// Pooled keys are added up under this power of two (exact, down to the smallest scale), so that the sum of
+// up to 8192 keys is finite where their mean is.
+constexpr float kPoolUnit = 0x1p-14f;
 constexpr uint32_t kInfBits = 0x7f80;  // magnitude bits of a bf16 infinity; NaN lies above
 
 template <int kFmt>
@@ -269,7 +272,7 @@ struct PageRows {
   }
 };
 
-// acc += scale * (sum of the stored codes of a whole page), as the rows above are spread.
+// acc += kPoolUnit * scale * (sum of the stored codes of a whole page), as the rows above are spread.
 template <int kD, int kFmt, int kThreads>
 __device__ __forceinline__ void add_stored_page(const CacheGeom& g, const uint8_t* slab, float scale, float (&acc)[8]) {
   constexpr int kVec = kD / 8, kRows = kThreads / kVec;
@@ -281,7 +284,7 @@ __device__ __forceinline__ void add_stored_page(const CacheGeom& g, const uint8_
     sum.template add4<4>(c.y);
   }
 #pragma unroll
-  for (int e = 0; e < 8; ++e) acc[e] = fmaf(sum.sum(e), scale, acc[e]);
+  for (int e = 0; e < 8; ++e) acc[e] = fmaf(sum.sum(e), scale * kPoolUnit, acc[e]);
 }
 
 // The CTA's sums of its columns (kN of them in each lane): part[d] for all d < kD, visible after the
@@ -361,7 +364,7 @@ __global__ void __launch_bounds__(kStepThreads)
         if ((threadIdx.x & 31) == 0) atomicOr(g.err, kErrBadPage);
         continue;
       }
-      const float scale = a.scales[(size_t)page * g.Hkv + head];
+      const float scale = a.scales[(size_t)page * g.Hkv + head] * kPoolUnit;
       const uint4* src = reinterpret_cast<const uint4*>(a.codes + slab_offset(g, page, head)) + v;
       CodeSums<kFmt, 16> sum;
 #pragma unroll 8
@@ -377,7 +380,7 @@ __global__ void __launch_bounds__(kStepThreads)
     }
     fold_columns<kD, 16, kStepThreads>(acc, sm);
     if (threadIdx.x < kD)
-      Kbar[(((size_t)s * g.MB + b) * g.Hkv + head) * kD + threadIdx.x] = sm.part[threadIdx.x] / (float)g.bs;
+      Kbar[(((size_t)s * g.MB + b) * g.Hkv + head) * kD + threadIdx.x] = sm.part[threadIdx.x] / (kPoolUnit * (float)g.bs);
   }
 }
 
@@ -511,7 +514,7 @@ __global__ void __launch_bounds__(prompt_threads(kPS), kPS == 128 ? 3 : 6)
         CodeSums<kFmt, 8> sum;
         const float scale = rows.template store<true>(nr, off, slab, sp, sm.red, turn, sum);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = fmaf(sum.sum(e), scale, acc[e]);
+        for (int e = 0; e < 8; ++e) acc[e] = fmaf(sum.sum(e), scale * kPoolUnit, acc[e]);
       } else {
         CodeSums<kFmt, 8> unused;
         if (page >= 0) rows.template store<false>(nr, off, slab, sp, sm.red, turn, unused);
@@ -532,7 +535,7 @@ __global__ void __launch_bounds__(prompt_threads(kPS), kPS == 128 ? 3 : 6)
     if (rank == 0 && threadIdx.x < kD) {
       float total = sm.part[threadIdx.x];
       for (int r = 1; r < ranks; ++r) total += ld_cluster_f32(&sm.part[threadIdx.x], r);
-      Kbar[(((size_t)s * g.MB + b) * g.Hkv + head) * kD + threadIdx.x] = total / (float)g.bs;
+      Kbar[(((size_t)s * g.MB + b) * g.Hkv + head) * kD + threadIdx.x] = total / (kPoolUnit * (float)g.bs);
     }
     cluster_barrier();  // no CTA goes on while its share is read
   }
