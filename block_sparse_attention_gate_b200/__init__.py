@@ -318,8 +318,11 @@ class MobaCacheParams:
                  softmax_scale: float = 0.0):
         if format not in CACHE_FORMATS:
             raise MobaError(2, "format must be one of %s (got %r)" % (", ".join(CACHE_FORMATS), format))
-        self.c = _CCacheParams(max_seqs, max_seqlen, num_pages, page_size, num_q_heads, num_kv_heads, head_dim,
-                               block_size, top_k, CACHE_FORMATS[format], softmax_scale)
+        sizes = (max_seqs, max_seqlen, num_pages, page_size, num_q_heads, num_kv_heads, head_dim, block_size, top_k)
+        for (name, _), n in zip(_CCacheParams._fields_, sizes):
+            if not -(1 << 31) <= n < 1 << 31:  # ctypes would take it modulo 2^32
+                raise MobaError(2, "%s does not fit in 32 bits (got %d)" % (name, n))
+        self.c = _CCacheParams(*sizes, CACHE_FORMATS[format], softmax_scale)
         self._ref = ctypes.byref(self.c)
         self.format = format
         # an append of no tokens checks the parameters and does nothing else
@@ -393,6 +396,8 @@ class MobaCacheParams:
     def _slots(self, index, slots):
         if slots.dim() != 1 or slots.dtype is not self.buffers["slots"][0] or slots.get_device() != index or not slots.is_contiguous():
             self._check_one("slots", slots, index)
+        if slots.shape[0] >= 1 << 31:
+            raise MobaError(2, "slots must have less than 2^31 entries (got %d)" % slots.shape[0])
         return slots.data_ptr()
 
 
