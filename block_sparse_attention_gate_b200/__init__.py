@@ -374,7 +374,7 @@ class MobaCacheParams:
             if t.device != device:
                 raise MobaError(1, "%s is on %s, the call's tensors are on %s" % (name, t.device, device))
             if name in ("K", "V"):
-                if t.shape[0] and (t.stride(2) != 1 or t.stride(1) != t.shape[2]):
+                if t.shape[0] and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
                     raise MobaError(1, "%s must be contiguous in its last two dimensions" % name)
             elif not t.is_contiguous():
                 raise MobaError(1, "%s must be contiguous" % name)
