@@ -317,8 +317,9 @@ struct AppendSide {
   float* scales;
 };
 
-// Page that a token goes to: its slot has to be at the token's offset in a page of the pool; -1 if it
-// is left out.
+// Page that a request's run of new tokens in one page goes to, by the slot of the first of them, which has
+// to be at that token's offset in a page of the pool; -1 if the run is left out.  The other slots of a run
+// follow from it and are not read.
 __device__ __forceinline__ int32_t page_of_slot(const CacheGeom& g, int32_t slot, int off) {
   if (slot < 0) return -1;
   if (slot % g.ps == off && page_ok(g, slot / g.ps)) return slot / g.ps;

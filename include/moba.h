@@ -293,8 +293,10 @@ MOBA_API moba_status moba_fwd_host(const moba_params* p, const void* Q, const vo
  *
  * A page id outside [0, num_pages), a length outside [0, max_seqlen] and a slot that does not
  * fit its token never lead to an access: such tokens are left out (read as masked, not written),
- * and page ids and slots set bit 2 of the device error word (moba_read_device_error).  A negative
- * slot is skipped without an error.
+ * and page ids and slots OR 2 into the device error word (moba_read_device_error).  Of the slots
+ * of a run, a request's new tokens in one page, the first decides for all of them: where it does
+ * not fit (it is not at its token's offset in a page of the pool) the run is left out, where it is
+ * negative the run is left out without an error, and otherwise the run is written behind it.
  */
 typedef enum {
   MOBA_CACHE_E4M3 = 0, /* fp8 e4m3: values to 4 significant bits, largest code 448 */
@@ -347,7 +349,8 @@ MOBA_API moba_status moba_cache_tables(const moba_cache_params* p, const int32_t
  *   K, V     [max_tokens, Hkv, D] bf16, the requests' new tokens packed in the order of s; rows
  *            k_stride (v_stride) elements apart, a multiple of 8 and at least Hkv * D (K and V
  *            may be slices of one projection).  Rows behind cu_new[max_seqs] are not read.
- *   cu_new, slots  from moba_cache_tables;  lens  the lengths AFTER the step (its lens_out).
+ *   cu_new, slots  from moba_cache_tables (of slots, the first of each run is read);  lens  the
+ *            lengths AFTER the step (its lens_out).
  *   Scale of a (page, KV head) with qmax = 448 (e4m3) or 127 (int8): the least number of 8
  *   significant bits that is >= max(2^-96, max |x|) / qmax over the finite new values, or the old
  *   scale if the page held tokens and that is larger.  When a page's scale grows, its older codes
