@@ -15,7 +15,8 @@
 // latency for single tokens.  Two forms of one body:
 //   cache_append_kernel : a CTA for each (request, KV head, K or V) takes the request's touched
 //                         pages one after the other: for requests with few new tokens (2.7 us for
-//                         single tokens of 8, 5.8 us for 64 of which some complete a block of 512).
+//                         single tokens of 8, 5.8 us for 64 of which some complete a block of 512,
+//                         45 us where all 64 complete a block of 2048 of 8 heads of 128).
 //   cache_prompt_kernel : for requests with the tokens of kLongPages pages or more, a cluster of up to 8
 //                         CTAs for each (touched MoBA block, some KV heads, K or half of V); its CTAs
 //                         share the block's pages and add up the pooled key on the way (54769 tokens, 8
@@ -582,11 +583,13 @@ cudaError_t launch_append_t(const CacheGeom& g, const AppendSide& sk, const Appe
                             const int32_t* cu_new, const int32_t* lens, const int32_t* slots, const int32_t* tables,
                             float* Kbar, cudaStream_t st) {
   // Where a request has two pages of new tokens on average, all go as prompts; else those with fewer than
-  // kLongPages one page after the other and then the others, where there can be any (with up to 4 tokens
-  // a slot, as decode steps and drafts have, there hardly are).  Pages of 64, 8 heads of 128, us one page
+  // kLongPages one page after the other and then the others, where there can be any.  Up to 4 tokens a slot
+  // count as decode steps and drafts, without long runs: the second launch would cost them 2 to 3 us (10.1
+  // and 12.8 for 256 tokens in one of 256 slots).  A long run among so many slots is slow by that: 1024
+  // tokens in one of 256 slots 25 us, 13 with the second launch; 4000 in one of 1000 101 and 37.  Pages of 64, 8 heads of 128, us one page
   // after the other / all as prompts / by this rule: 1 request with 256 tokens 11.6 / 7.7 / 7.7; 24 with
   // 300 31 / 27 / 27; 64 with 600 76 / 75 / 75; 64 with 16 8.9 / 33 / 11.4; one with 8000 beside 63 with one
-  // 181 / 42 / 26.  The rule loses where many requests have a few pages each: 32 with 128 15 / 26 / 26, 64
+  // 181 / 42 / 26.  The rule also loses where many requests have a few pages each: 32 with 128 15 / 26 / 26, 64
   // with 256 41 / 53 / 53.  Limits of 8 pages for full grids give 19 and 48 us there, but 35 for 24 with 300
   // and 35 instead of 31 for 32 with 256.
   const int32_t tokens = kLongPages * g.ps;

@@ -244,10 +244,10 @@ __global__ void __launch_bounds__(kGateWarps * 32)
 //  - The k index of the products runs through a lane's own bytes, so both operands come out of the
 //    swizzled tiles by 16-byte reads without bank conflicts; only the weights change places between
 //    lanes (movmatrix).
-// Measured (32/8 heads of 128, blocks of 2048, top_k 3, e4m3): 281 MB of eight 128K caches in 52 us (5.5
-// TB/s, start and tail included), 2.3 GB of 64 of them at 6.2 TB/s, what a copy reaches.  At D 64 the
-// conversions and the softmax of half as many bytes a key bound it: 156 MB of 37 ragged int8 caches in
-// 45 us, issue slots 48 % busy.
+// Measured (32/8 heads of 128, blocks of 2048, top_k 3, e4m3): 281 MB of eight 128K caches in 51 us (5.5
+// TB/s, start and tail included), 2.3 GB of 64 of them at 6.2 TB/s, what a copy reaches.  At D 64 there is
+// half the memory traffic for a key's conversions and softmax, and their latencies bound it: 156 MB of 37
+// ragged int8 caches in 46 us, issue slots 48 % busy with three warps on a scheduler.
 
 constexpr float kNoScore = -1e38f;  // reference before the first key: finite, below every score that counts
 constexpr int kPiece = 256;     // keys whose pages a warp holds at a time (at most 16 pages)
@@ -996,7 +996,8 @@ cudaError_t launch_decode_t(const CacheGeom& g, const __nv_bfloat16* Q, const ui
 // take 385 us at 1024 keys, 403 at 256 (32/8 heads of 128, top_k 3 of blocks of 2048); 37 ragged ones of
 // 64 dimensions 51 us at 256, 58 at 512 (blocks of 512).  With fewer, a bit more than half as many units
 // as warps have enough copies on their way to fill the memory: eight caches of 128K take 57 us at 1024
-// keys, 64 at 256; one of 1M 21 us at 256, 22 at 128, 28 at 512.
+// keys (what the rule takes), 67 at 256; one of 1M 22.5 us at 128 (the rule), 21.6 at 256, 28 at 512.  The
+// work space's size follows from this on the host, without a device, so the SMs are those of a B200.
 int cache_chunk_keys(const CacheGeom& g) {
   const int64_t entries = (int64_t)g.B * g.Hkv * ((g.G + 7) / 8);
   const int64_t past = (int64_t)(g.k - 1) * (1 + (g.G < 8 ? g.G : 8)) / 2;

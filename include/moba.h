@@ -378,6 +378,11 @@ MOBA_API moba_status moba_cache_append(const moba_cache_params* p, const void* K
  *   O     [max_seqs, Hq, D] bf16 out;  LSE [max_seqs, Hq] fp32 out.
  *   A request of length 0 gets sel = -1, O = 0 and LSE = -inf.
  * Whatever stands in a page behind the newest token is without effect.
+ * Precision: logits, the softmax's sum and the weighted values are summed in fp32.  For the value
+ * product each weight is rounded to fp16 relative to the largest weight times value scale, to
+ * within 2^-11 of itself or 2^-25 of that largest one, so that O before its rounding to bf16 is
+ * within (2^-10 + what the logits' fp32 rounding adds) * sum_j p_j |v_j|; LSE does not depend on
+ * the weights in fp16.  Q is taken exactly down to 2^-32 of its head's largest element.
  */
 MOBA_API size_t moba_cache_decode_workspace_size(const moba_cache_params* p);
 MOBA_API moba_status moba_cache_decode_fwd(const moba_cache_params* p, const void* Q, const void* Kc, const void* Vc,
