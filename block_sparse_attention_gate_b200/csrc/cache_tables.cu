@@ -15,8 +15,9 @@
 // size; several chunks take a first pass for the totals, which decide whether the call changes
 // anything); the pages and tokens are then spread over the cluster's threads, each of which finds its
 // request by bisection in the scanned offsets in shared memory.  Lengths and the ring's state may be
-// updated in place, so they are written behind a barrier of the cluster.  4.0 us for one token of 64
-// requests, 9.7 us for 128K tokens of 16 prompts in pages of 16, 7.9 us for 20011 tokens of 1000 requests.
+// updated in place, so they are written behind a barrier of the cluster.  4.2 us for one token of 64
+// requests, 10.0 us for 128K tokens of 16 prompts in pages of 16, 8.1 us for 20011 tokens of 1000 requests
+// (0.1 to 0.2 of it to count the pages held).
 #include "moba.h"
 #include "cache.cuh"
 #include "sm100.cuh"
