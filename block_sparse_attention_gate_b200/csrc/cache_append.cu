@@ -586,12 +586,12 @@ cudaError_t launch_append_t(const CacheGeom& g, const AppendSide& sk, const Appe
   // kLongPages one page after the other and then the others, where there can be any.  Up to 4 tokens a slot
   // count as decode steps and drafts, without long runs: the second launch would cost them 2 to 3 us (10.1
   // and 12.8 for 256 tokens in one of 256 slots).  A long run among so many slots is slow by that: 1024
-  // tokens in one of 256 slots 25 us, 13 with the second launch; 4000 in one of 1000 101 and 37.  Pages of 64, 8 heads of 128, us one page
-  // after the other / all as prompts / by this rule: 1 request with 256 tokens 11.6 / 7.7 / 7.7; 24 with
-  // 300 31 / 27 / 27; 64 with 600 76 / 75 / 75; 64 with 16 8.9 / 33 / 11.4; one with 8000 beside 63 with one
-  // 181 / 42 / 26.  The rule also loses where many requests have a few pages each: 32 with 128 15 / 26 / 26, 64
-  // with 256 41 / 53 / 53.  Limits of 8 pages for full grids give 19 and 48 us there, but 35 for 24 with 300
-  // and 35 instead of 31 for 32 with 256.
+  // tokens in one of 256 slots 25 us, 13 with the second launch; 4000 in one of 1000 101 and 37.
+  // Pages of 64, 8 heads of 128, us one page after the other / all as prompts / by this rule: 1 request with
+  // 256 tokens 11.6 / 7.7 / 7.7; 24 with 300 31 / 27 / 27; 64 with 600 76 / 75 / 75; 64 with 16 8.9 / 33 /
+  // 11.4; one with 8000 beside 63 with one 181 / 42 / 26.  The rule also loses where many requests have a few
+  // pages each: 32 with 128 15 / 26 / 26, 64 with 256 41 / 53 / 53.  Limits of 8 pages for full grids give 19
+  // and 48 us there, but 35 for 24 with 300 and 35 instead of 31 for 32 with 256.
   const int32_t tokens = kLongPages * g.ps;
   const bool prompts = max_tokens >= 2 * (int64_t)g.ps * g.B;
   const bool few = max_tokens < tokens || max_tokens <= 4 * (int64_t)g.B;
