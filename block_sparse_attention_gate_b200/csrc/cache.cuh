@@ -85,7 +85,7 @@ struct CacheDecodeWork {
   CacheSeg* segs;    // [entries, max_segs] distinct blocks, the own one last
   int32_t* units;    // [entries] chunks in all
   float* part_o;     // [B, Hq, k, NC, D] partial sums of weighted values
-  float4* part_ml;   // [B, Hq, k, NC] references of the weights and of the softmax's sum (log2 units), that sum
+  float4* part_ml;   // [B, Hq, k, NC] references r and u (log2 units), sum of the softmax
   int32_t* sel;      // [B, Hq, k] (used when the caller passes none)
   int32_t max_segs, CK, NC;
   size_t bytes;

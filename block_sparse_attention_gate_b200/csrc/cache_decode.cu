@@ -236,11 +236,12 @@ __global__ void __launch_bounds__(kGateWarps * 32)
 // first, and these instructions are busy for 18 % of the time that the codes take to arrive.
 //  - Q is scaled by a power of two for each head and held in fp16: exact down to 2^-32 of the head's
 //    largest element.
-//  - The value scale enters through the exponent, w_j = 2^(z_j + log2 Vs - M) with M the maximum of
-//    z_j + log2 Vs so far, or up to 8 less: fp16 weights are relative to the largest CONTRIBUTION,
-//    however far the pages' scales lie apart (rounding 2^-11 of each weight).  The sum of the softmax
-//    takes 2^(z_j - R) in fp32, with R the maximum of z_j so far, or up to 8 less: log2 Vs may lie
-//    anywhere from -105 (a page of zeros) to 121, so relative to M the sum would overflow or vanish.
+//  - The sum of the softmax takes 2^(z_j - r) in fp32, with r the maximum of z_j so far, or up to 8 less.
+//  - The value scale enters through the exponent, w_j = 2^((z_j - r) + (log2 Vs - u)) with u the maximum
+//    of (z_j - r) + log2 Vs so far, or up to 8 less: fp16 weights are relative to the largest
+//    CONTRIBUTION, however far the pages' scales lie apart (rounding 2^-11 of each weight).  log2 Vs may
+//    lie anywhere from -105 (a page of zeros) to 121, so relative to that the sum would overflow or vanish.
+//    z_j is rounded before r is taken off, which is then exact for the largest z_j, whatever their size.
 //  - The k index of the products runs through a lane's own bytes, so both operands come out of the
 //    swizzled tiles by 16-byte reads without bank conflicts; only the weights change places between
 //    lanes (movmatrix).
@@ -547,7 +548,7 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
   float sf[2];                  // of heads 2t, 2t + 1: softmax scale over Q's power of two, log2 units
   int q_idx = -1;
   float o[kW][4], l[2];         // l: sum of the softmax
-  float m[2], r[2];             // references of the weights in o and of those in l (below)
+  float r[2], u[2];             // references (below)
   bool fresh = true;            // nothing is added up yet
 
   while (true) {
@@ -586,8 +587,8 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
       for (int j = 0; j < kW; ++j)
 #pragma unroll
         for (int x = 0; x < 4; ++x) o[j][x] = 0.f;
-      m[0] = m[1] = r[0] = r[1] = kNoScore;
-      l[0] = l[1] = 0.f;
+      r[0] = r[1] = kNoScore;
+      u[0] = u[1] = l[0] = l[1] = 0.f;
       fresh = true;
     }
     const float lvs = log2f(vs);
@@ -641,65 +642,63 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
             v[mt][x][0] = u.x, v[mt][x][1] = u.y;
           }
         }
-      // ---- online softmax: z = c * f, and with the value scale z + lv
+      // ---- online softmax: z = c * f, in place of c
       int live[kMT] = {};  // keys of each 16 that count
-      float f0[kMT], f1[kMT], lv[kMT], mx0 = -INFINITY, mx1 = -INFINITY;
+      float f0, f1, lv[kMT], zx0 = -INFINITY, zx1 = -INFINITY;
 #pragma unroll
       for (int mt = 0; mt < kMT; ++mt) {
         const int key = tile * kTile + mt * 16, pi = (offset_of(cur) + key) >> lps & 31;
         if (mt > 0 && box == kTile) {  // the same page
           lv[mt] = lv[0];
-          f0[mt] = f0[0];
-          f1[mt] = f1[0];
         } else {
           const float k1 = __shfl_sync(0xffffffffu, ks, pi);
           lv[mt] = __shfl_sync(0xffffffffu, lvs, pi);
-          f0[mt] = k1 * sf[0];
-          f1[mt] = k1 * sf[1];
+          f0 = k1 * sf[0];
+          f1 = k1 * sf[1];
         }
         if constexpr (kOdd) {
           const int32_t pg = __shfl_sync(0xffffffffu, page_c, pi);
           live[mt] = pg >= 0 ? min(16, cur.n - key) : 0;
         }
-      }
-      auto masked = [&](int mt, int x) { return kOdd && (x < 2 ? gq : gq + 8) >= live[mt]; };
-      // c * f, plus what is added to it; -inf for a masked key
-      auto score = [&](int mt, int x, float plus) {
-        const float v = fmaf(c[mt][x], x & 1 ? f1[mt] : f0[mt], plus);
-        return masked(mt, x) ? -INFINITY : v;
-      };
 #pragma unroll
-      for (int mt = 0; mt < kMT; ++mt) {
-        mx0 = max3(mx0, score(mt, 0, lv[mt]), score(mt, 2, lv[mt]));
-        mx1 = max3(mx1, score(mt, 1, lv[mt]), score(mt, 3, lv[mt]));
-      }
-      // m and r are maxima of earlier keys, not the largest so far: weights up to 2^kSlack are as good in fp16
-      // and fp32, and the exact maxima over the lanes are only needed when a key leaves that range.  A tile's
-      // largest z is at most its largest z + lv less its smallest lv.
-      constexpr float kSlack = 8.f;
-      const float lv_min = kMT > 1 && box != kTile ? fminf(lv[0], lv[kMT - 1]) : lv[0];
-      if (__any_sync(0xffffffffu, mx0 > fminf(m[0], r[0] + lv_min) + kSlack || mx1 > fminf(m[1], r[1] + lv_min) + kSlack)) {
-        float zx0 = -INFINITY, zx1 = -INFINITY;
-#pragma unroll
-        for (int mt = 0; mt < kMT; ++mt) {
-          zx0 = max3(zx0, score(mt, 0, 0.f), score(mt, 2, 0.f));
-          zx1 = max3(zx1, score(mt, 1, 0.f), score(mt, 3, 0.f));
+        for (int x = 0; x < 4; ++x) {
+          c[mt][x] = __fmul_rn(c[mt][x], x & 1 ? f1 : f0);
+          if (kOdd && (x < 2 ? gq : gq + 8) >= live[mt]) c[mt][x] = -INFINITY;  // masked
         }
+        zx0 = max3(zx0, c[mt][0], c[mt][2]);
+        zx1 = max3(zx1, c[mt][1], c[mt][3]);
+      }
+      // r and u are maxima of earlier keys, not the largest so far: weights up to 2^kSlack are as good in fp16
+      // and fp32, and the exact maxima over the lanes are only needed when a key may leave that range
+      constexpr float kSlack = 8.f;
+      const float lv_max = kMT > 1 && box != kTile ? fmaxf(lv[0], lv[kMT - 1]) : lv[0];
+      if (__any_sync(0xffffffffu, zx0 - r[0] > fminf(u[0] - lv_max, 0.f) + kSlack ||
+                                      zx1 - r[1] > fminf(u[1] - lv_max, 0.f) + kSlack)) {
 #pragma unroll
         for (int off = 4; off <= 16; off <<= 1) {
-          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
-          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
           zx0 = fmaxf(zx0, __shfl_xor_sync(0xffffffffu, zx0, off));
           zx1 = fmaxf(zx1, __shfl_xor_sync(0xffffffffu, zx1, off));
         }
-        mx0 = fmaxf(mx0, m[0]);
-        mx1 = fmaxf(mx1, m[1]);
         zx0 = fmaxf(zx0, r[0]);
         zx1 = fmaxf(zx1, r[1]);
+        float ux0 = -INFINITY, ux1 = -INFINITY;
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt) {
+          ux0 = fmaxf(ux0, fmaxf(c[mt][0] - zx0, c[mt][2] - zx0) + lv[mt]);
+          ux1 = fmaxf(ux1, fmaxf(c[mt][1] - zx1, c[mt][3] - zx1) + lv[mt]);
+        }
+#pragma unroll
+        for (int off = 4; off <= 16; off <<= 1) {
+          ux0 = fmaxf(ux0, __shfl_xor_sync(0xffffffffu, ux0, off));
+          ux1 = fmaxf(ux1, __shfl_xor_sync(0xffffffffu, ux1, off));
+        }
+        const float d0 = r[0] - zx0, d1 = r[1] - zx1;  // the old references under the new r
+        ux0 = fmaxf(ux0, d0 + u[0]);
+        ux1 = fmaxf(ux1, d1 + u[1]);
         if (!fresh) {
-          const float a0 = ex2(m[0] - mx0), a1 = ex2(m[1] - mx1);
-          l[0] *= ex2(r[0] - zx0);
-          l[1] *= ex2(r[1] - zx1);
+          const float a0 = ex2(d0 + u[0] - ux0), a1 = ex2(d1 + u[1] - ux1);
+          l[0] *= ex2(d0);
+          l[1] *= ex2(d1);
 #pragma unroll
           for (int j = 0; j < kW; ++j) {
             o[j][0] *= a0;
@@ -708,20 +707,22 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
             o[j][3] *= a1;
           }
         }
-        m[0] = mx0;
-        m[1] = mx1;
         r[0] = zx0;
         r[1] = zx1;
+        u[0] = ux0;
+        u[1] = ux1;
       }
       fresh = false;
       // ---- O += V^T P: dimensions of group gq, heads 2t and 2t + 1
 #pragma unroll
       for (int mt = 0; mt < kMT; ++mt) {
-        l[0] += ex2(score(mt, 0, -r[0])) + ex2(score(mt, 2, -r[0]));
-        l[1] += ex2(score(mt, 1, -r[1])) + ex2(score(mt, 3, -r[1]));
-        const float w0 = lv[mt] - m[0], w1 = lv[mt] - m[1];
-        const uint32_t p0 = transpose8(pack_half2(ex2(score(mt, 0, w0)), ex2(score(mt, 1, w1))));
-        const uint32_t p1 = transpose8(pack_half2(ex2(score(mt, 2, w0)), ex2(score(mt, 3, w1))));
+#pragma unroll
+        for (int x = 0; x < 4; ++x) c[mt][x] -= r[x & 1];
+        l[0] += ex2(c[mt][0]) + ex2(c[mt][2]);
+        l[1] += ex2(c[mt][1]) + ex2(c[mt][3]);
+        const float w0 = lv[mt] - u[0], w1 = lv[mt] - u[1];
+        const uint32_t p0 = transpose8(pack_half2(ex2(c[mt][0] + w0), ex2(c[mt][1] + w1)));
+        const uint32_t p1 = transpose8(pack_half2(ex2(c[mt][2] + w0), ex2(c[mt][3] + w1)));
         if constexpr (kOdd) {
 #pragma unroll
           for (int x = 0; x < 4; ++x)
@@ -772,7 +773,7 @@ __global__ void __launch_bounds__(AttnLayout<kD>::kWarps * 32, 1)
           float4* dst = reinterpret_cast<float4*>(w.part_o + part * kD + gq * (kD / 8));
 #pragma unroll
           for (int j = 0; j < kW; j += 2) dst[j / 2] = make_float4(o[j][e], o[j][2 + e], o[j + 1][e], o[j + 1][2 + e]);
-          if (gq == 0) w.part_ml[part] = make_float4(m[e], r[e], ls[e], 0.f);
+          if (gq == 0) w.part_ml[part] = make_float4(r[e], u[e], ls[e], 0.f);
         }
       }
     }
@@ -836,17 +837,22 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   };
   wait_for_primary();
   fetch(0);  // while the weights are found
-  float M = kNoScore, R = kNoScore;
-  for (int x = lane; x < n; x += 32) {
+  // R: largest r; U: largest (r - R) + u, the reference of acc.  Up to 64 parts are read once for both.
+  float4 held[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x)
+    held[x] = lane + 32 * x < n ? __ldcg(ml + at(lane + 32 * x)) : make_float4(kNoScore, 0.f, 0.f, 0.f);
+  float R = fmaxf(held[0].x, held[1].x);
+  for (int x = lane + 64; x < n; x += 32) R = fmaxf(R, __ldcg(ml + at(x)).x);
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) R = fmaxf(R, __shfl_xor_sync(0xffffffffu, R, off));
+  float U = fmaxf((held[0].x - R) + held[0].y, (held[1].x - R) + held[1].y);
+  for (int x = lane + 64; x < n; x += 32) {
     const float4 v = __ldcg(ml + at(x));
-    M = fmaxf(M, v.x);
-    R = fmaxf(R, v.y);
+    U = fmaxf(U, (v.x - R) + v.y);
   }
 #pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) {
-    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    R = fmaxf(R, __shfl_xor_sync(0xffffffffu, R, off));
-  }
+  for (int off = 16; off >= 1; off >>= 1) U = fmaxf(U, __shfl_xor_sync(0xffffffffu, U, off));
   float L = 0.f, acc[kDL];
 #pragma unroll
   for (int d = 0; d < kDL; ++d) acc[d] = 0.f;
@@ -854,8 +860,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     float wt = 0.f;
     if (x0 + lane < mine) {
       const float4 v = __ldcg(ml + at(part + (x0 + lane) * kWarps));
-      wt = ex2(v.x - M);
-      L = fmaf(v.z, ex2(v.y - R), L);
+      wt = ex2((v.x - R) + v.y - U);
+      L = fmaf(v.z, ex2(v.x - R), L);
     }
     for (int x1 = x0; x1 < min(mine, x0 + 32); x1 += kMergeRows) {
       if (x1 > 0) fetch(x1);
@@ -885,7 +891,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   }
   if (!live) return;
   const float inv = L == 0.f ? 0.f : 1.f / L;  // 0: no key at all
-  const float up = ex2(0.5f * (M - R));  // root of what the weights of acc carry of the value scales (up to 2^129)
+  const float up = ex2(0.5f * U);  // root of what the weights of acc carry of the value scales (up to 2^129)
 #pragma unroll
   for (int d = 0; d < kDL; d += 2)
     *reinterpret_cast<__nv_bfloat162*>(O + row * kD + lane * kDL + d) =

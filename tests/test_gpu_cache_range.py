@@ -80,3 +80,46 @@ def test_many_keys_without_values(ps, D, low, fmt, cuda_device):
     _check_decode(p, pool, q, kbar, lens, pool.tab, got)
     assert (got[0] == 0).all()
     _no_error()
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("exponent", [6, 12, 16, 24, 50])
+@pytest.mark.parametrize("ps,Hq,H,D,bs,k", [(16, 4, 2, 64, 128, 4), (64, 3, 1, 128, 256, 3), (128, 16, 1, 64, 512, 2)])
+def test_logits_of_any_magnitude(ps, Hq, H, D, bs, k, exponent, fmt, cuda_device):
+    """Queries and keys times 2^exponent each, logits from about 2^12 to 2^100.  Where the best logit leads by
+    more than 64 times what fp32 rounds (half a step, for D products and a few factors), every other weight is below
+    e^-20 of it (the lead is at least 60): O is the best key's value and LSE its logit, to their roundings."""
+    import block_sparse_attention_gate_b200 as mb
+    rng = np.random.default_rng(exponent * ps)
+    B, max_len = 4, 2000
+    P = B * -(-max_len // ps)
+    p = mb.MobaCacheParams(B, max_len, P, ps, Hq, H, D, bs, k, fmt)
+    pool = Pool(rng, B, max_len, P, ps, H, D, fmt)
+    pool.Ks *= 2.0 ** exponent
+    kbar = _kbar_of(pool, B, max_len, ps, bs, H, D)
+    lens = np.array([2000, 1, 2 * ps, 1111])
+    q = _bf16(rng.standard_normal((B, Hq, D)) * 2.0 ** exponent)
+    O, LSE, sel = (t.double().cpu().numpy() for t in _decode(p, pool, q, kbar, lens, pool.tab))
+    _no_error()
+    assert np.isfinite(O).all() and np.isfinite(LSE).all()
+    kc, vc, ks, vs = pool.values()
+    qf, led = q.double().cpu().numpy(), 0
+    want_sel = ref.decode(qf, kc, vc, ks, vs, kbar.double().cpu().numpy(), lens, pool.tab, ps, bs, k, D ** -0.5)[2]
+    np.testing.assert_array_equal(sel, want_sel)
+    for s in range(B):
+        for h in range(Hq):
+            blocks = [int(b) for b in want_sel[s, h] if b >= 0]
+            pos = np.concatenate([np.arange(b * bs, min((b + 1) * bs, lens[s])) for b in blocks])
+            page, g = pool.tab[s, pos // ps], h // (Hq // H)
+            key = kc[page, g, pos % ps] * ks[page, g, None]
+            z, zabs = key @ qf[s, h] * D ** -0.5, (np.abs(key) @ np.abs(qf[s, h])).max() * D ** -0.5
+            order, dz = np.argsort(-z), (D + 8) * 2.0 ** -24 * zabs
+            lead = z[order[0]] - z[order[1]] if len(z) > 1 else np.inf
+            assert abs(LSE[s, h] - z[order[0]]) <= dz + 4 * 2.0 ** -24 * zabs + np.log(len(z))
+            if lead < 60 or lead < 64 * dz:
+                continue
+            led += 1
+            top = order[0]
+            v, rest = vc[page[top], g, pos[top] % ps] * vs[page[top], g], np.abs(vc).max() * vs.max() * 2e-9 * len(z)
+            assert np.all(np.abs(O[s, h] - v) <= (2.0 ** -8 + 2.0 ** -10) * np.abs(v) + rest)
+    assert led >= B  # the request of one token leads by itself
