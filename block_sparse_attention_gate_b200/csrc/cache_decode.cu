@@ -245,10 +245,10 @@ __global__ void __launch_bounds__(kGateWarps * 32)
 //  - The k index of the products runs through a lane's own bytes, so both operands come out of the
 //    swizzled tiles by 16-byte reads without bank conflicts; only the weights change places between
 //    lanes (movmatrix).
-// Measured (32/8 heads of 128, blocks of 2048, top_k 3, e4m3): 281 MB of eight 128K caches in 51 us (5.5
+// Measured (32/8 heads of 128, blocks of 2048, top_k 3, e4m3): 281 MB of eight 128K caches in 53 us (5.4
 // TB/s, start and tail included), 2.3 GB of 64 of them at 6.2 TB/s, what a copy reaches.  At D 64 there is
 // half the memory traffic for a key's conversions and softmax, and their latencies bound it: 156 MB of 37
-// ragged int8 caches in 46 us, issue slots 48 % busy with three warps on a scheduler.
+// ragged int8 caches in 48 us, issue slots 47 % busy with three warps on a scheduler.
 
 constexpr float kNoScore = -1e38f;  // reference before the first key: finite, below every score that counts
 constexpr int kPiece = 256;     // keys whose pages a warp holds at a time (at most 16 pages)
